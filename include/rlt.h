@@ -319,6 +319,129 @@ uint32_t rlt_build_flags(void);
 int rlt_debug_set_positions(rlt_state* state, int row, int32_t pos_enc, int32_t pos_dec,
                             void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged 8-bit key/value cache (no counterpart in the method: serving memory
+ * for long prefixes and large batches).
+ *
+ * Keys and values are e4m3 bytes (1 sign, 4 exponent, 3 mantissa bits; largest
+ * 448) in pages of `page` tokens; every (page, head) has one fp32 scale for its
+ * keys and one for its values, and a byte x stands for x * scale:
+ *   pages  e4m3 [n_pages][2][kv_heads][page][dh]   (index 0: K, 1: V)
+ *   scales fp32 [n_pages][2][kv_heads]             (positive and finite)
+ *   table  int32 [rows][row_pages]                 token j of row b sits in page
+ *          table[b][j / page], slot j % page.
+ * All buffers are caller-owned device memory, `pages` aligned to 16 bytes; the
+ * struct itself is host memory, read during the call only.  page is 16, 32, 64
+ * or 128; dh is 64 or 128; n_pages times the bytes of a page may pass 2^32.
+ * status (device int32, may be NULL) is a sticky word the kernels set to the
+ * first problem they meet, which they step around: RLT_E_ARG, a table entry
+ * outside [0, n_pages) (append: the tokens of that block are not written;
+ * attend: its keys are not seen); RLT_E_CAPACITY, a length below 0 or above
+ * row_pages * page, or a position without a row in the rotation table (append:
+ * those tokens are not written; attend: a length is cut to the capacity, a
+ * query without a rotation gives 0).  The caller zeroes it.
+ * Table entries of blocks past a row's length are not read.  Pages may be
+ * shared between rows for reading; a page that two rows of one append write
+ * is undefined.
+ *
+ * These calls, rlt_beam_select and rlt_rows_reorder take no model or state.
+ * They allocate nothing, use no scratch, keep nothing from call to call, read
+ * lengths and tables on the device (so a captured call may be replayed with
+ * new ones) and return with the calling thread's current device unchanged.
+ * They run on the device that holds `pages` (the logits; the rows); every
+ * buffer must be on that device and `stream` belong to it, else RLT_E_ARG.
+ * RLT_E_ARG also for null or misaligned pointers, sizes below 1 (a call for
+ * 0 rows or tokens does nothing), a type other than the two named;
+ * RLT_E_UNSUPPORTED for a page or head size other than those above. */
+typedef struct rlt_cache8 {
+    void* pages;
+    float* scales;
+    const int32_t* table;
+    int32_t* status;
+    int32_t n_pages, rows, row_pages, page, kv_heads, dh;
+} rlt_cache8;
+
+/* Rotary positions: cos and sin (device fp32 [positions][rot/2], aligned to 16
+ * bytes) of the angles of positions 0, 1, ...; the first `rot` dimensions of
+ * each head (a multiple of 8, at most dh) are rotated in pairs, (j, j + rot/2)
+ * or, with interleaved != 0, (2j, 2j+1):
+ *   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s).
+ * Token j of a row has position j + origin (origin 1: this library's 1-based
+ * positions).  Scalings for long contexts are the table's. */
+typedef struct rlt_rope {
+    const float* cos;
+    const float* sin;
+    int32_t positions, rot, interleaved, origin;
+} rlt_rope;
+
+/* Append: row b's tokens i < counts[b] (counts NULL: all n; a count outside
+ * [0, n] is RLT_E_CAPACITY in status, and the row is left as it was) become
+ * tokens start[b] + i of the cache, their keys rotated first when rope is not
+ * NULL.  k, v: `dtype` (RLT_DTYPE_F32 or _BF16) [rows][n][kv_heads][dh] with
+ * row and token pitches in elements, heads adjacent; pitches and addresses
+ * multiples of 16 bytes.  start, counts: device int32 [rows].
+ * The scale of a (page, head) is the smallest power of two, at least 2^-110,
+ * that brings the largest magnitude of the tokens written to at most 448; a
+ * page that already holds tokens of the row (start[b] inside it) keeps the
+ * larger of its scale and the new one, its bytes brought to it (exactly, but
+ * for magnitudes below 2^-6 of a scale, which round again).  Values are
+ * rounded to nearest even after the rotation, whose products and sums are
+ * rounded in fp32 one by one.  NaN stays NaN; infinities become +-448 scales
+ * and count as the largest finite value. */
+int rlt_cache8_append(const rlt_cache8* cache, int dtype, const void* k, int64_t k_row,
+                      int64_t k_token, const void* v, int64_t v_row, int64_t v_token,
+                      const int32_t* start, const int32_t* counts, int n, const rlt_rope* rope,
+                      void* stream);
+
+/* Attention of n queries per row over the row's first lens[b] tokens: query i
+ * (the block's i-th newest-to-be: token lens[b] - n + i of the row) sees the
+ * tokens 0 .. lens[b] - n + i; one that sees none gives 0.  heads is a
+ * multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
+ *   out = softmax(scale * q . k) v, q rotated at its token's position when
+ * rope is not NULL.  q, out: `dtype` [rows][n][heads][dh] with row and token
+ * pitches in elements, heads adjacent, 16-byte multiples as above; out must not
+ * overlap q.  lens: device int32 [rows].  Scores, the softmax and the sums are
+ * fp32; with more than 8 query vectors per key head (n * heads / kv_heads) and
+ * bf16 types, the probabilities enter the value product as fp16.  A row's
+ * result does not depend on the other rows, on `rows` or on row_pages, bit for
+ * bit.  NaN in a value makes at least that dimension of the queries that see
+ * it NaN, and of no others. */
+int rlt_cache8_attend(const rlt_cache8* cache, int dtype, const void* q, int64_t q_row,
+                      int64_t q_token, void* out, int64_t out_row, int64_t out_token, int heads,
+                      int n, const int32_t* lens, float scale, const rlt_rope* rope,
+                      void* stream);
+
+/* Beam search's selection.  For every group (search) of `beams` rows of
+ * logits (`dtype` fp32 or bf16, [groups][beams][vocab], dense, no alignment
+ * beyond the element's) the candidates are, per beam b and token v,
+ *   c(b, v) = scores[b] + log softmax(logits_b / temperature)[v],
+ * and for a beam with finished[b] != 0 (uint8, NULL: none) the single candidate
+ * (b, eos) with score scores[b].  The k largest go out in descending order,
+ * equal ones by ascending b * vocab + v: parents (the beam within the group),
+ * tokens, new_scores [groups][k]; new_finished (uint8, may be NULL) is 1 where
+ * the parent was finished or the token is eos (eos < 0: no token is).  Scores
+ * are compared and formed in fp64 and rounded once.  A logit of -inf or NaN is
+ * no candidate, nor is anything of a beam whose score is not finite (its
+ * logits are not read: the empty beams of a search's first token) or that has
+ * a +inf logit; when fewer than k candidates are left, the remaining outputs
+ * are parent 0, token 0, score -inf, not finished.  Outputs may not overlap
+ * inputs.  1 <= beams, k <= 64, vocab < 2^24, k <= beams * vocab; temperature
+ * in [2^-20, 2^20]; finished needs 0 <= eos < vocab. */
+int rlt_beam_select(int dtype, const void* logits, const float* scores, const uint8_t* finished,
+                    int eos, float temperature, int groups, int beams, int vocab, int k,
+                    int32_t* parents, int32_t* tokens, float* new_scores, uint8_t* new_finished,
+                    void* stream);
+
+/* Reorders the rows of one buffer within groups of `beams` (1 .. 64), in
+ * place: row g*beams + i takes the contents that row g*beams + parents[g][i]
+ * had before the call, in bytes [offset, offset + bytes) of each of its
+ * `planes` planes (plane_stride apart; rows row_stride apart).  parents:
+ * device int32 [groups][beams]; an index outside [0, beams) leaves its row as
+ * it was.  Any alignment; 16-byte multiples everywhere run fastest. */
+int rlt_rows_reorder(void* rows, const int32_t* parents, int groups, int beams, int64_t row_stride,
+                     int planes, int64_t plane_stride, int64_t offset, int64_t bytes,
+                     void* stream);
+
 /* Number of kernels this library has launched in this process. */
 uint64_t rlt_kernel_launches(void);
 

@@ -48,8 +48,26 @@ class rlt_config(ctypes.Structure):
                [("alpha", ctypes.c_double), ("eps", ctypes.c_double), ("rope_base", ctypes.c_double)]
 
 
+class rlt_cache8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "scales", "table", "status")] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "rows", "row_pages", "page", "kv_heads",
+                                              "dh")]
+
+
+class rlt_rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cos", "sin")] + \
+               [(n, ctypes.c_int32) for n in ("positions", "rot", "interleaved", "origin")]
+
+
 _vp, _i, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
 _SIGS = {
+    "rlt_cache8_append": (_i, [_vp, _i, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _vp, _vp]),
+    "rlt_cache8_attend": (_i, [_vp, _i, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _vp, _f32, _vp,
+                               _vp]),
+    "rlt_beam_select": (_i, [_i, _vp, _vp, _vp, _i, _f32, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
+                             _vp]),
+    "rlt_rows_reorder": (_i, [_vp, _vp, _i, _i, _i64, _i, _i64, _i64, _i64, _vp]),
     "rlt_create": (_i, [_vp, _sz, _i, ctypes.POINTER(_vp)]),
     "rlt_destroy": (None, [_vp]),
     "rlt_model_config": (_i, [_vp, ctypes.POINTER(rlt_config)]),
@@ -88,7 +106,7 @@ for _name, (_res, _args) in _SIGS.items():
 def header_functions() -> list:
     """Names of the functions include/rlt.h declares."""
     src = open(HEADER_PATH).read()
-    return sorted(set(re.findall(r"\b(rlt_[a-z_]+)\s*\(", src)))
+    return sorted(set(re.findall(r"\b(rlt_[a-z0-9_]+)\s*\(", src)))
 
 
 class RLTError(RuntimeError):
@@ -307,6 +325,167 @@ def rlt_profile_query(state, cls: int, stream=None):
     code = _lib.rlt_profile_query(state, cls, ctypes.byref(n), ctypes.byref(ms), ctypes.byref(by),
                                   _stream(stream))
     return code, n.value, ms.value, by.value
+
+
+# ---------------------------------------------------------------- operators on the caller's buffers
+DTYPE_F32, DTYPE_BF16 = 0, 1               # RLT_DTYPE_*
+_DTYPES = {"float32": DTYPE_F32, "bfloat16": DTYPE_BF16}
+
+
+def _device_buf(x, what: str, dtypes, shape=None, device=None):
+    """Address of a CUDA tensor after its type, shape (None: any extent) and
+    device are checked; strides are the caller's to check."""
+    if not getattr(x, "is_cuda", False):
+        raise TypeError(f"{what}: expected a CUDA tensor, got {type(x).__name__}"
+                        f"{' on the host' if hasattr(x, 'data_ptr') else ''}")
+    name = str(x.dtype).replace("torch.", "")
+    if name not in dtypes:
+        raise TypeError(f"{what}: element type {name}, expected {' or '.join(dtypes)}")
+    if shape is not None and (len(x.shape) != len(shape) or
+                              any(b is not None and a != b for a, b in zip(x.shape, shape))):
+        raise ValueError(f"{what}: shape {tuple(x.shape)}, expected "
+                         f"({', '.join('*' if b is None else str(b) for b in shape)})")
+    if device is not None and x.device != device:
+        raise ValueError(f"{what}: on {x.device}, expected {device}")
+    return x.data_ptr()
+
+
+def _dense(x, what: str, *args, **kw):
+    p = _device_buf(x, what, *args, **kw)
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return p
+
+
+def _heads_tensor(x, what: str, dtypes, shape, device):
+    """Address, row pitch and token pitch of a [rows][n][heads][dh] tensor whose heads are
+    adjacent."""
+    p = _device_buf(x, what, dtypes, shape, device)
+    row, token, head, one = x.stride()
+    if x.numel() and (one != 1 or (head != shape[3] and shape[2] > 1)):
+        raise ValueError(f"{what}: the last two dimensions must be contiguous, strides "
+                         f"{tuple(x.stride())}")
+    return p, row, token
+
+
+class Rope:
+    """Rotary positions: cos and sin fp32 [positions][rot/2] CUDA tensors (rlt_rope).  Token j of a
+    row has position j + origin."""
+
+    def __init__(self, cos, sin, interleaved: bool = False, origin: int = 0):
+        positions, half = (int(n) for n in cos.shape)
+        self.buffers = (cos, sin)
+        self.device = cos.device
+        self.struct = rlt_rope(_dense(cos, "cos", ("float32",)),
+                               _dense(sin, "sin", ("float32",), (positions, half), cos.device),
+                               positions, 2 * half, int(bool(interleaved)), origin)
+
+
+class Cache8:
+    """A paged 8-bit key/value cache over the caller's CUDA tensors (rlt_cache8):
+    pages uint8 or float8_e4m3fn [n_pages][2][kv_heads][page][dh], scales fp32
+    [n_pages][2][kv_heads], table int32 [rows][row_pages]; status (optional) int32 [1], zeroed by
+    the caller.  The tensors are kept alive and used in place, never copied."""
+
+    def __init__(self, pages, scales, table, status=None):
+        p = _dense(pages, "pages", ("uint8", "float8_e4m3fn"), (None, 2, None, None, None))
+        n_pages, _, kv_heads, page, dh = (int(n) for n in pages.shape)
+        self.device = pages.device
+        s = _dense(scales, "scales", ("float32",), (n_pages, 2, kv_heads), self.device)
+        t = _dense(table, "table", ("int32",), (None, None), self.device)
+        w = None if status is None else _dense(status, "status", ("int32",), (1,), self.device)
+        self.pages, self.scales, self.table, self.status = pages, scales, table, status
+        self.rows, self.row_pages = (int(n) for n in table.shape)
+        self.kv_heads, self.page, self.dh = kv_heads, page, dh
+        self.struct = rlt_cache8(p, s, t, w, n_pages, self.rows, self.row_pages, page, kv_heads, dh)
+        self._ref = ctypes.byref(self.struct)
+
+    def _rope(self, rope):
+        if rope is None:
+            return None
+        if rope.device != self.device:
+            raise ValueError(f"rope: on {rope.device}, expected {self.device}")
+        return ctypes.byref(rope.struct)
+
+    def append(self, k, v, start, counts=None, rope: Optional[Rope] = None, stream=None):
+        """Append k, v ([rows][n][kv_heads][dh] fp32 or bf16; row and token strides are free) at
+        tokens start[b] .. start[b]+counts[b]-1 (int32 [rows]; counts None: n each), k rotated
+        first when rope is given."""
+        n = int(k.shape[1]) if len(k.shape) == 4 else 0
+        shape = (self.rows, n, self.kv_heads, self.dh)
+        kp, kr, kt = _heads_tensor(k, "k", _DTYPES, shape, self.device)
+        name = str(k.dtype).replace("torch.", "")
+        vp, vr, vt = _heads_tensor(v, "v", (name,), shape, self.device)
+        sp = _dense(start, "start", ("int32",), (self.rows,), self.device)
+        cp = None if counts is None else _dense(counts, "counts", ("int32",), (self.rows,),
+                                                self.device)
+        return _check(_lib.rlt_cache8_append(self._ref, _DTYPES[name], kp, kr, kt, vp, vr, vt, sp,
+                                             cp, n, self._rope(rope), _stream(stream)),
+                      "rlt_cache8_append")
+
+    def attend(self, q, lens, out, scale: Optional[float] = None, rope: Optional[Rope] = None,
+               stream=None):
+        """out = attention of q ([rows][n][heads][dh]) over each row's first lens[b] tokens, query i
+        seeing tokens 0 .. lens[b] - n + i; scale defaults to 1/sqrt(dh)."""
+        n, heads = (int(q.shape[1]), int(q.shape[2])) if len(q.shape) == 4 else (0, 0)
+        shape = (self.rows, n, heads, self.dh)
+        qp, qr, qt = _heads_tensor(q, "q", _DTYPES, shape, self.device)
+        name = str(q.dtype).replace("torch.", "")
+        op, o_r, ot = _heads_tensor(out, "out", (name,), shape, self.device)
+        lp = _dense(lens, "lens", ("int32",), (self.rows,), self.device)
+        if scale is None:
+            scale = self.dh ** -0.5
+        return _check(_lib.rlt_cache8_attend(self._ref, _DTYPES[name], qp, qr, qt, op, o_r, ot,
+                                             heads, n, lp, scale, self._rope(rope),
+                                             _stream(stream)), "rlt_cache8_attend")
+
+
+def beam_select(logits, scores, parents, tokens, new_scores, finished=None, new_finished=None,
+                eos: int = -1, temperature: float = 1.0, stream=None):
+    """The k best continuations of each group's beams (rlt_beam_select): logits fp32 or bf16
+    [groups][beams][vocab], scores fp32 [groups][beams], finished uint8 [groups][beams]; outputs
+    parents and tokens int32, new_scores fp32, new_finished uint8, each [groups][k]."""
+    lp = _dense(logits, "logits", _DTYPES, (None, None, None))
+    groups, beams, vocab = (int(n) for n in logits.shape)
+    dev = logits.device
+    pp = _dense(parents, "parents", ("int32",), (groups, None), dev)
+    k = int(parents.shape[1])
+    opt = lambda x, what, shape: None if x is None else _dense(  # noqa: E731
+        x, what, ("uint8",), shape, dev)
+    return _check(_lib.rlt_beam_select(
+        _DTYPES[str(logits.dtype).replace("torch.", "")], lp,
+        _dense(scores, "scores", ("float32",), (groups, beams), dev),
+        opt(finished, "finished", (groups, beams)), eos, temperature, groups, beams, vocab, k, pp,
+        _dense(tokens, "tokens", ("int32",), (groups, k), dev),
+        _dense(new_scores, "new_scores", ("float32",), (groups, k), dev),
+        opt(new_finished, "new_finished", (groups, k)), _stream(stream)), "rlt_beam_select")
+
+
+def rows_reorder(rows, parents, start: int = 0, stop: Optional[int] = None, stream=None):
+    """Reorder the rows of a tensor in place (rlt_rows_reorder): rows [groups*beams][planes][cap]
+    [width] of any element type, the last two dimensions contiguous, parents int32
+    [groups][beams]; positions [start, stop) of every plane of row g*beams + i take what row
+    g*beams + parents[g][i] held."""
+    pp = _dense(parents, "parents", ("int32",), (None, None))
+    groups, beams = (int(n) for n in parents.shape)
+    if not getattr(rows, "is_cuda", False):
+        raise TypeError("rows: expected a CUDA tensor")
+    if rows.device != parents.device:
+        raise ValueError(f"rows: on {rows.device}, expected {parents.device}")
+    if len(rows.shape) != 4 or int(rows.shape[0]) != groups * beams:
+        raise ValueError(f"rows: shape {tuple(rows.shape)}, expected ({groups * beams}, *, *, *)")
+    _, planes, cap, width = (int(n) for n in rows.shape)
+    stop = cap if stop is None else stop
+    if not 0 <= start <= stop <= cap:
+        raise ValueError(f"rows: positions [{start}, {stop}) of {cap}")
+    row, plane, pos, one = rows.stride()
+    if rows.numel() and ((one != 1 and width > 1) or (pos != width and cap > 1)):
+        raise ValueError(f"rows: the last two dimensions must be contiguous, strides {rows.stride()}")
+    elt = rows.element_size()
+    return _check(_lib.rlt_rows_reorder(rows.data_ptr(), pp, groups, beams, row * elt, planes,
+                                        plane * elt, start * width * elt,
+                                        (stop - start) * width * elt, _stream(stream)),
+                  "rlt_rows_reorder")
 
 
 # ---------------------------------------------------------------- owners

@@ -95,6 +95,8 @@ void set_carveout_once(const void* kernel);
 // The kernel's dynamic shared-memory limit, set once per (device, kernel,
 // size); false when the device refuses it.
 bool set_smem_once(const void* kernel, size_t bytes);
+// Allows clusters of 16 CTAs, once per (device, kernel); false when refused.
+bool set_wide_cluster_once(const void* kernel);
 // Multiprocessors of the current device (0 on error).
 int sm_count();
 

@@ -81,6 +81,18 @@ bool set_smem_once(const void* kernel, size_t bytes) {
     g_attr_done.insert(key);
     return true;
 }
+bool set_wide_cluster_once(const void* kernel) {
+    std::lock_guard<std::mutex> lk(g_attr_mu);
+    const auto key = std::make_tuple(current_device(), kernel, -2);
+    if (g_attr_done.count(key)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    g_attr_done.insert(key);
+    return true;
+}
 int sm_count() {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, current_device()) !=
