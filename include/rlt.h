@@ -401,7 +401,7 @@ int rlt_cache8_append(const rlt_cache8* cache, int dtype, const void* k, int64_t
  * rope is not NULL.  q, out: `dtype` [rows][n][heads][dh] with row and token
  * pitches in elements, heads adjacent, 16-byte multiples as above; out must not
  * overlap q.  lens: device int32 [rows].  Scores, the softmax and the sums are
- * fp32; with more than 8 query vectors per key head (n * heads / kv_heads) and
+ * fp32; with more than 4 query vectors per key head (n * heads / kv_heads) and
  * bf16 types, the probabilities enter the value product as fp16.  A row's
  * result does not depend on the other rows, on `rows` or on row_pages, bit for
  * bit.  NaN in a value makes at least that dimension of the queries that see

@@ -9,16 +9,22 @@
 // scalars per head, and w stays within fp16's range whatever the scales.
 //
 // Matrix form.  One warp takes 16 keys at a time through m16n8k16 fp16
-// products with fp32 sums: a single decoded token fills one row of 16, but
-// converting a byte pair to fp16 is one instruction where multiplying it in
-// fp32 on the CUDA cores would take four, so the tensor cores carry the
-// per-key work of an HBM stream.  The unused rows buy precision: up to 8
-// query vectors per key head (SPLIT) occupy rows 0-7 with the leading 11 bits
-// of q (of w), rows 8-15 with the next 11 bits times 2^11, and the two rows'
-// sums are added in fp32.  More than 8 bf16 queries fill 16 rows with the
-// leading bits alone: a bf16 q is exact there (each row is brought near 1 by
-// a power of two first), w is rounded to fp16 (2^-11 relative at most, below
-// the bf16 output's 2^-9 step); fp32 types always run SPLIT.
+// products with fp32 sums, keys (then value dims) as the 16 rows, queries as
+// the 8 columns: converting a byte pair to fp16 is one instruction where
+// multiplying it in fp32 on the CUDA cores would take four, so the tensor
+// cores carry the per-key work of an HBM stream even for one query.  (Queries
+// as rows, tried first, need twice the products and twice the registers of
+// the output: 618 instructions per 4 KB tile and 12 warps an SM, 2.5 TB/s on 64
+// rows x 16 heads x 4.3k keys.)  Columns left over buy precision:
+//   FOLD   up to 4 query vectors per key head: columns 0-3 hold the leading 11
+//          bits of q (of w), columns 4-7 the next 11 bits times 2^11, and the two
+//          sums are added in fp32;
+//   SPLIT  up to 8, fp32 types: the same in two products;
+//   PLAIN  8 or 16 bf16 queries, leading bits alone: a bf16 q is exact there
+//          (each query is brought near 1 by a power of two first), w is rounded
+//          to fp16 (2^-11 relative at most, below the bf16 output's 2^-9 step).
+// The weights pass from the score product's layout to the value product's
+// operand by an 8x8 transpose of the warp's registers (movmatrix).
 //
 // The maximum is raised only when a score passes it by 2^8 (one warp vote per
 // tile instead of a reduction); fp16 holds weights up to 2^16.
@@ -26,19 +32,19 @@
 // Data path.  Tiles reach a per-warp ring in shared memory by 16-byte
 // cp.async copies; keys past the prefix and keys in bad pages are zero-filled
 // rather than read, so whatever bytes sit there never enter a product.  Key
-// rows and 16-byte chunks are permuted on the way in (krow, kchunk, vchunk)
-// so that every fragment load is one conflict-free wide load: lane (g, t) =
-// (lane/4, lane%4) reads dims [t D/4, (t+1) D/4) of its key and of its query
-// row, and dims [g D/8, (g+1) D/8) of values 4i+t.
+// rows and 16-byte chunks are permuted on the way in so that every fragment
+// load is one conflict-free wide load: lane (g, t) = (lane/4, lane%4) reads
+// dims [t D/4, (t+1) D/4) of key rows g and g + 8 and of query g, and dims
+// [g D/8, (g+1) D/8) of values 4i + t; key row r holds key
+// sigma(r) = (r & 8) + 4 (r & 1) + (r & 7) / 2, the order the transpose wants.
 //
 // Split.  The prefix of a (row, key head) is cut into runs for 4 warps of
-// ceil(keys / 1024) CTAs (at most 16), a function of that prefix alone.  The
+// 2^j <= keys / 1024 CTAs (1 to 16), a function of that prefix alone.  The
 // warps' partial results meet in shared memory, the CTAs' through the
 // cluster's distributed shared memory, always in run order: no scratch, no
 // atomics, and the same bits for a row whatever batch or capacity it sits in.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
@@ -80,11 +86,22 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// two e4m3 bytes (the low 16 bits) as two fp16 values, exactly
-__device__ __forceinline__ uint32_t h2_of(uint32_t two) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// four e4m3 bytes as two pairs of fp16 values, exactly (NaN stays NaN)
+__device__ __forceinline__ void h2x2_of(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n"
+        ".reg .b16 a, b;\n"
+        "mov.b32 {a, b}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n"
+        "}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+// the transpose of an 8x8 matrix of fp16 held two to a lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -151,32 +168,30 @@ __device__ __forceinline__ void load_q4(const QIn<TQ>& q, size_t at, int d, cons
     }
 }
 
-// where key row r of a tile and its 16-byte chunk c go in shared memory
-template <int D>
-__device__ __forceinline__ uint32_t k_at(int r, int c) {
-    const int pr = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
-    return (uint32_t)(pr * D + ((D == 128 ? c ^ (pr & 1) : c) << 4));
-}
-template <int D>
-__device__ __forceinline__ uint32_t v_at(int r, int c) {
-    return (uint32_t)(r * D + ((D == 128 ? c ^ ((r & 3) << 1) : c ^ (r & 2)) << 4));
-}
-
 template <int D> constexpr int stages() { return D == 64 ? 4 : 3; }
 template <int D> constexpr int stage_bytes() { return 2 * kTile * D + 16; }
 template <int D> constexpr int ring_bytes() { return kWarps * stages<D>() * stage_bytes<D>(); }
 
-struct Tile8 {              // per-page scalars of a tile, beside it in the ring
-    float ks, lv, inv;      // key scale, log2 of the value scale, 1 / value scale
-};
+enum Mode { FOLD, SPLIT, PLAIN };
+constexpr int queries_of(int mode, int nb) { return mode == FOLD ? 4 : mode == SPLIT ? 8 : 8 * nb; }
 
-template <int D, bool SPLIT, typename TQ, typename TO>
+// CTAs that share a prefix of `keys` keys: a power of two, kKeysPerCta keys each at least
+__host__ __device__ __forceinline__ int ctas_of(int64_t keys) {
+    int c = 1;
+    while (c < kMaxCtas && (int64_t)c * 2 * kKeysPerCta <= keys) c *= 2;
+    return c;
+}
+
+// MODE and NB (products of 8 columns): FOLD 1, SPLIT 2, PLAIN 1 or 2
+template <int D, int MODE, int NB, typename TQ, typename TO>
 __global__ void __launch_bounds__(kWarps * 32)
 k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int q_tiles,
                 const int32_t* __restrict__ lens, int lens_add, float scale_log2e, Rope8 rope) {
-    constexpr int MT = SPLIT ? 8 : 16;      // query vectors per tile
-    constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 8;
+    constexpr int QT = queries_of(MODE, NB);    // query vectors per tile
+    constexpr int NS = MODE == PLAIN ? NB : 1;  // column tiles of scores: queries 8 b + 2t + e
+    constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float s_q[QT][D + 4];
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -191,10 +206,10 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const int L = max(0, min(cap, L0));
     if ((L0 < 0 || L0 > cap) && threadIdx.x == 0 && kvh == 0 && mt == 0 && rank == 0 && c.status)
         atomicCAS(c.status, 0, c.cap_code);
-    const int r0 = mt * MT, r_last = min(nq, r0 + MT) - 1;
-    const int vis_max = max(0, L - n + r_last / share + 1);   // keys any query of the tile sees
-    const int vis_min = L - n + r0 / share + 1;               // keys all of them see
-    const int nC = min(C, min(kMaxCtas, max(1, (vis_max + kKeysPerCta - 1) / kKeysPerCta)));
+    const int r0 = mt * QT, live = min(QT, nq - r0);
+    const int vis_max = max(0, L - n + (r0 + live - 1) / share + 1);  // keys any query of the tile sees
+    const int vis_min = L - n + r0 / share + 1;                      // keys all of them see
+    const int nC = min(C, ctas_of(vis_max));
     if (rank >= nC) return;
     const int subs = (vis_max + kTile - 1) / kTile, runs = nC * kWarps;
     const int per = (subs + runs - 1) / runs;
@@ -204,6 +219,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     uint8_t* ring = smem + warp * (NST * SB);
     const uint32_t ring_u = tc::smem_u32(ring);
     const size_t head_bytes = (size_t)D << page_log2;
+    const size_t v_bytes = (size_t)c.kv_heads * head_bytes;
     int b_base = s_begin;                   // first tile of the batch below
     int b_page = -1;                        // lane l: the page of tile b_base + l, and its scalars
     float b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
@@ -225,6 +241,19 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             }
         }
     };
+    // a lane copies chunk ch of rows cr, cr + RS, ...; where they go in a stage
+    constexpr int CPR = D / 16, RS = 32 / CPR, NK = kTile / RS;     // chunks per row, rows per pass
+    const int cr = lane / CPR, ch = lane % CPR;
+    uint32_t k_off[2], v_off;
+    if constexpr (D == 128) {               // rows cr + 4k -> 2 cr + (k & 1) + 8 (k / 2)
+        k_off[0] = (uint32_t)(2 * cr * D + ch * 16);
+        k_off[1] = (uint32_t)((2 * cr + 1) * D + (ch ^ 1) * 16);
+        v_off = (uint32_t)(kTile * D + cr * D + (ch ^ (cr << 1)) * 16);
+    } else {                                // rows cr + 8k -> 2 (cr & 3) + cr / 4 + 8k
+        k_off[0] = (uint32_t)((((cr & 3) << 1) | (cr >> 2)) * D + ch * 16);
+        k_off[1] = k_off[0] + 8 * D;
+        v_off = (uint32_t)(kTile * D + cr * D + (ch ^ (cr & 2)) * 16);
+    }
     auto issue = [&](int i) {               // tile s_begin + i into stage i % NST
         const int s = s_begin + i;
         if (s < s_end) {
@@ -242,16 +271,17 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 *reinterpret_cast<float4*>(ring + slot * SB + 2 * kTile * D) =
                     make_float4(ks, lv, inv, 0.f);
             const uint8_t* kg = c.pages + ((size_t)max(p, 0) * 2 * c.kv_heads + kvh) * head_bytes +
-                                (size_t)(k0 & ((1 << page_log2) - 1)) * D;
-            const uint8_t* vg = kg + (size_t)c.kv_heads * head_bytes;
+                                (size_t)(k0 & ((1 << page_log2) - 1)) * D + lane * 16;
+            const uint8_t* vg = kg + v_bytes;
             const int left = p >= 0 ? vis_max - k0 : 0;
             const uint32_t at = ring_u + slot * SB;
+            const bool whole = left >= kTile;
 #pragma unroll
-            for (int x = lane; x < D; x += 32) {        // D chunks of 16 bytes each
-                const int r = x / (D / 16), ch = x % (D / 16);
-                const bool ok = r < left;
-                cp16(at + k_at<D>(r, ch), ok ? kg + x * 16 : c.pages, ok);
-                cp16(at + kTile * D + v_at<D>(r, ch), ok ? vg + x * 16 : c.pages, ok);
+            for (int k = 0; k < NK; ++k) {
+                const uint32_t kd = D == 128 ? k_off[k & 1] + (k >> 1) * 8 * D : k_off[k];
+                const bool ok = whole || cr + k * RS < left;
+                cp16(at + kd, ok ? kg + k * 512 : c.pages, ok);
+                cp16(at + v_off + k * RS * D, ok ? vg + k * 512 : c.pages, ok);
             }
         }
         cp_commit();
@@ -261,68 +291,92 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     for (int i = 0; i < NST - 1; ++i) issue(i);
 
     // ---------------------------------------------------------------- queries
-    // rows g (and, 16 rows, g + 8): this lane's dims [t D/4, (t+1) D/4)
-    uint32_t qf[KI][4];
-    float rf[SPLIT ? 1 : 2];                // score factor of the row: 2^e scale log2(e)
-    int vis[SPLIT ? 1 : 2];                 // keys it sees
-#pragma unroll
-    for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-        const int r = r0 + g + 8 * w;
-        const int i = r / share, pos = L - n + i + rope.origin;
-        float x[KI][4];
-        float amax = 0.f;
-        vis[w] = r < nq ? max(0, L - n + i + 1) : 0;
-        if (vis[w] > 0 && rope.rot && (pos < 0 || pos >= rope.positions)) {
-            if (c.status) atomicCAS(c.status, 0, c.cap_code);
-            vis[w] = 0;
+    // rotated once per CTA, then split into operands by every warp
+    for (int x = threadIdx.x; x < QT * (D / 4); x += kWarps * 32) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < live) {
+            const int rr = r0 + r, i = rr / share, pos = L - n + i + rope.origin;
+            const bool seen = L - n + i >= 0;
+            const bool lost = seen && rope.rot && (pos < 0 || pos >= rope.positions);
+            if (lost && d == 0 && c.status) atomicCAS(c.status, 0, c.cap_code);
+            if (seen && !lost) {
+                const size_t at = (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
+                                  (size_t)(kvh * share + rr % share) * D;
+                load_q4(q, at, d, rope, pos, y);
+            }
         }
+        *reinterpret_cast<float4*>(&s_q[r][d]) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    // column g of product b: this lane's dims [t D/4, (t+1) D/4) of its query
+    uint32_t qf[KI][NB][2];
+    float rf[NS][2];                        // score factor of queries 2t, 2t+1: 2^e scale log2(e)
+    int vis[NS][2];                         // keys they see
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (MODE == SPLIT && b == 1) break;
+        const int r = MODE == FOLD ? g & 3 : 8 * b + g;
+        const float* sq = &s_q[r][t * (D / 4)];
+        float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < KI; ++k) {
-            if (vis[w] > 0) {
-                const size_t at = (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
-                                  (size_t)(kvh * share + r % share) * D;
-                load_q4(q, at, t * (D / 4) + 4 * k, rope, pos, x[k]);
-            } else {
-                x[k][0] = x[k][1] = x[k][2] = x[k][3] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+            const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
+            amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // bring the row near 1 by a power of two (exact); 2^±100 bounds keep both factors finite
+        // bring the query near 1 by a power of two (exact); 2^+-100 keeps both factors finite
         int e2 = (int)(__float_as_uint(amax) >> 23) - 127;
         e2 = max(-100, min(100, e2));
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-        rf[w] = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
+        const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
+        const bool low = MODE == FOLD && g >= 4;
 #pragma unroll
         for (int k = 0; k < KI; ++k) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[k][e] *= down;
-            const uint32_t h0 = pack_h2(x[k][0], x[k][1]), h1 = pack_h2(x[k][2], x[k][3]);
-            if (SPLIT) {
-                qf[k][0] = h0;
-                qf[k][2] = h1;
-                qf[k][1] = rest_h2(x[k][0], x[k][1], h0);
-                qf[k][3] = rest_h2(x[k][2], x[k][3], h1);
-            } else {
-                qf[k][0 + w] = h0;
-                qf[k][2 + w] = h1;
+            const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
+            const float x0 = x.x * down, x1 = x.y * down, x2 = x.z * down, x3 = x.w * down;
+            const uint32_t h0 = pack_h2(x0, x1), h1 = pack_h2(x2, x3);
+            qf[k][b][0] = h0;
+            qf[k][b][1] = h1;
+            if (MODE == FOLD && low) {
+                qf[k][b][0] = rest_h2(x0, x1, h0);
+                qf[k][b][1] = rest_h2(x2, x3, h1);
+            }
+            if (MODE == SPLIT) {
+                qf[k][NB - 1][0] = rest_h2(x0, x1, h0);
+                qf[k][NB - 1][1] = rest_h2(x2, x3, h1);
             }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = (2 * t + e) & (MODE == FOLD ? 3 : 7);
+            rf[b][e] = __shfl_sync(0xffffffffu, up, 4 * col);
+            const int rr = r0 + 8 * b + col, i = rr / share, pos = L - n + i + rope.origin;
+            vis[b][e] = rr < nq ? max(0, L - n + i + 1) : 0;
+            if (rope.rot && (pos < 0 || pos >= rope.positions)) vis[b][e] = 0;
+        }
     }
-
-    // a query without a rotation sees nothing: its row has to be masked from the first key on
-    const bool dead = vis[0] < min(vis_min, r0 + g < nq ? vis_min : 0) ||
-                      (!SPLIT && vis[SPLIT ? 0 : 1] < min(vis_min, r0 + g + 8 < nq ? vis_min : 0));
-    const int mask_from = __any_sync(0xffffffffu, dead) ? 0 : vis_min;
+    // a query without a rotation sees nothing: its column has to be masked from the first key on
+    bool lost = false;
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = (2 * t + e) & (MODE == FOLD ? 3 : 7);
+            lost |= 8 * b + col < live && vis[b][e] < vis_min;
+        }
+    const int mask_from = __any_sync(0xffffffffu, lost) ? 0 : vis_min;
 
     // ---------------------------------------------------------------- the run
-    float m[SPLIT ? 1 : 2], l[SPLIT ? 1 : 2], O[VJ][4];
+    float m[NS][2], l[NS][2], O[VJ][NB][4];
 #pragma unroll
-    for (int w = 0; w < (SPLIT ? 1 : 2); ++w) m[w] = -INFINITY, l[w] = 0.f;
+    for (int b = 0; b < NS; ++b) m[b][0] = m[b][1] = -INFINITY, l[b][0] = l[b][1] = 0.f;
 #pragma unroll
-    for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
+    for (int j = 0; j < VJ; ++j)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) O[j][b][0] = O[j][b][1] = O[j][b][2] = O[j][b][3] = 0.f;
+    const int key_lo = 4 * (g & 1) + (g >> 1);      // sigma(g): the key of row g; row g + 8: + 8
 
     for (int it = 0; s_begin + it < s_end; ++it) {
         cp_wait<NST - 2>();
@@ -332,19 +386,23 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         const float4 meta = *reinterpret_cast<const float4*>(st + 2 * kTile * D);
         const int k0 = (s_begin + it) * kTile;
 
-        float cf[2][4];
+        float cf[NB][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            cf[u][0] = cf[u][1] = cf[u][2] = cf[u][3] = 0.f;
-            const int pr = 8 * u + g;       // the permuted row that holds this lane's key
+        for (int b = 0; b < NB; ++b) cf[b][0] = cf[b][1] = cf[b][2] = cf[b][3] = 0.f;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                const int ch = D == 128 ? (2 * t + h) ^ (pr & 1) : t;
-                const uint4 kk = *reinterpret_cast<const uint4*>(st + pr * D + ch * 16);
-                mma_f16(cf[u], qf[4 * h + 0], h2_of(kk.x), h2_of(kk.x >> 16));
-                mma_f16(cf[u], qf[4 * h + 1], h2_of(kk.y), h2_of(kk.y >> 16));
-                mma_f16(cf[u], qf[4 * h + 2], h2_of(kk.z), h2_of(kk.z >> 16));
-                mma_f16(cf[u], qf[4 * h + 3], h2_of(kk.w), h2_of(kk.w >> 16));
+        for (int h = 0; h < D / 64; ++h) {
+            const int kc = D == 128 ? (2 * t + h) ^ (g & 1) : t;
+            const uint4 x = *reinterpret_cast<const uint4*>(st + g * D + kc * 16);
+            const uint4 y = *reinterpret_cast<const uint4*>(st + (g + 8) * D + kc * 16);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a[4];
+                h2x2_of(xs[k], a[0], a[2]);
+                h2x2_of(ys[k], a[1], a[3]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    mma_f16(cf[b], a, qf[4 * h + k][b][0], qf[4 * h + k][b][1]);
             }
         }
         // values 4i + t, dims [g D/8, (g+1) D/8)
@@ -361,32 +419,39 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 vv[i][0] = v2.x, vv[i][1] = v2.y;
             }
         }
-        // scores of keys 4i + t (i = 2u + e), the value scale folded in
-        float s[SPLIT ? 1 : 2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int u = i >> 1, e = i & 1;
-            if (SPLIT) {
-                s[0][i] = fmaf(fmaf(cf[u][2 + e], 1.f / 2048.f, cf[u][e]), rf[0] * meta.x, meta.y);
-            } else {
-                s[0][i] = fmaf(cf[u][e], rf[0] * meta.x, meta.y);
-                s[SPLIT ? 0 : 1][i] = fmaf(cf[u][2 + e], rf[SPLIT ? 0 : 1] * meta.x, meta.y);
-            }
-        }
-        const bool bad = !(meta.y > -INFINITY);
-        float poison[4] = {0.f, 0.f, 0.f, 0.f};
-        if (bad || k0 + kTile > mask_from) {  // the prefix ends in this tile for some query
+        // scores [key rows g, g + 8][queries 2t, 2t + 1], the value scale folded in
+        float s[NS][4];
+        if (MODE == FOLD) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = k0 + 4 * i + t;
-#pragma unroll
-                for (int w = 0; w < (SPLIT ? 1 : 2); ++w)
-                    if (bad || key >= vis[w]) s[w][i] = -INFINITY;
+                const float other = __shfl_xor_sync(0xffffffffu, cf[0][i], 2);
+                const float lead = t < 2 ? cf[0][i] : other, rest = t < 2 ? other : cf[0][i];
+                s[0][i] = fmaf(fmaf(rest, 1.f / 2048.f, lead), rf[0][i & 1] * meta.x, meta.y);
             }
+        } else if (MODE == SPLIT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[0][i] = fmaf(fmaf(cf[NB - 1][i], 1.f / 2048.f, cf[0][i]), rf[0][i & 1] * meta.x,
+                               meta.y);
+        } else {
+#pragma unroll
+            for (int b = 0; b < NS; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[b][i] = fmaf(cf[b][i], rf[b][i & 1] * meta.x, meta.y);
+        }
+        const bool bad = !(meta.y > -INFINITY);
+        uint32_t poison = 0;                // keys of the tile with a NaN among their values
+        if (bad || k0 + kTile > mask_from) {    // the prefix ends in this tile for some query
+#pragma unroll
+            for (int b = 0; b < NS; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (bad || k0 + key_lo + 8 * (i >> 1) >= vis[b][i & 1]) s[b][i] = -INFINITY;
             // A value seen by some queries only: a NaN in it would reach the others as
             // 0 x NaN, so it enters the product as 0 and the weights of those that see it
             // become NaN.
-            if (vis_min < vis_max) {
+            if (mask_from < vis_max) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t hit = 0;
@@ -396,134 +461,138 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                         hit |= z;
                         vv[i][x] &= ~((z >> 7) * 0xffu);
                     }
-                    const uint32_t any = __ballot_sync(0xffffffffu, hit != 0);
-                    if (any & (0x11111111u << t)) poison[i] = NAN;
+                    if (hit) poison |= 1u << (4 * i + t);
                 }
+                poison = __reduce_or_sync(0xffffffffu, poison);
             }
         }
-        float mx[SPLIT ? 1 : 2];
         bool raise = false;
+        float mx[NS][2];
 #pragma unroll
-        for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-            mx[w] = fmaxf(fmaxf(s[w][0], s[w][1]), fmaxf(s[w][2], s[w][3]));
-            raise |= mx[w] > m[w] + kLag;
-        }
+        for (int b = 0; b < NS; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[b][e] = fmaxf(s[b][e], s[b][2 + e]);
+                raise |= mx[b][e] > m[b][e] + kLag;
+            }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-                mx[w] = fmaxf(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], 1));
-                mx[w] = fmaxf(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], 2));
-                const float mn = fmaxf(m[w], mx[w]);
-                const float f = m[w] == mn ? 1.f : ex2(m[w] - mn);   // m = -inf: 0
-                m[w] = mn;
-                l[w] *= f;
+            for (int b = 0; b < NS; ++b)
 #pragma unroll
-                for (int j = 0; j < VJ; ++j) {
-                    if (SPLIT) {
-                        O[j][0] *= f, O[j][1] *= f, O[j][2] *= f, O[j][3] *= f;
-                    } else {
-                        O[j][2 * w] *= f, O[j][2 * w + 1] *= f;
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        mx[b][e] = fmaxf(mx[b][e], __shfl_xor_sync(0xffffffffu, mx[b][e], o));
+                    const float mn = fmaxf(m[b][e], mx[b][e]);
+                    const float f = m[b][e] == mn ? 1.f : ex2(m[b][e] - mn);    // m = -inf: 0
+                    m[b][e] = mn;
+                    l[b][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < VJ; ++j) {
+                        O[j][b][e] *= f, O[j][b][2 + e] *= f;
+                        if (MODE == SPLIT) O[j][NB - 1][e] *= f, O[j][NB - 1][2 + e] *= f;
                     }
                 }
-            }
         }
-        uint32_t a[4];
+        uint32_t pb[NB][2];                 // the value product's operand
 #pragma unroll
-        for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-            const float base = m[w] == -INFINITY ? 0.f : m[w];
+        for (int b = 0; b < NS; ++b) {
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = ex2(s[w][i] - base);
-                if (poison[i] != 0.f && s[w][i] != -INFINITY) p[i] = NAN;
-                l[w] = fmaf(p[i], meta.z, l[w]);
+                const float mm = m[b][i & 1];
+                p[i] = ex2(s[b][i] - (mm == -INFINITY ? 0.f : mm));
+                if (poison && s[b][i] != -INFINITY && ((poison >> (key_lo + 8 * (i >> 1))) & 1u))
+                    p[i] = NAN;
+                l[b][i & 1] = fmaf(p[i], meta.z, l[b][i & 1]);
             }
-            const uint32_t h0 = pack_h2(p[0], p[1]), h1 = pack_h2(p[2], p[3]);
-            if (SPLIT) {
-                a[0] = h0;
-                a[1] = rest_h2(p[0], p[1], h0);
-                a[2] = h1;
-                a[3] = rest_h2(p[2], p[3], h1);
-            } else {
-                a[0 + w] = h0;
-                a[2 + w] = h1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float p0 = p[2 * h], p1 = p[2 * h + 1];
+                const uint32_t lead = pack_h2(p0, p1);
+                if (MODE == FOLD) {
+                    pb[0][h] = transpose8(t < 2 ? lead : rest_h2(p0, p1, lead));
+                } else {
+                    pb[b][h] = transpose8(lead);
+                    if (MODE == SPLIT) pb[NB - 1][h] = transpose8(rest_h2(p0, p1, lead));
+                }
             }
         }
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
-            // bytes 4x .. 4x+3 of the four values, paired (key 0, key 1) and (key 2, key 3)
-            const uint32_t p0 = __byte_perm(vv[0][x], vv[1][x], 0x5140);
-            const uint32_t p1 = __byte_perm(vv[0][x], vv[1][x], 0x7362);
-            const uint32_t r0_ = __byte_perm(vv[2][x], vv[3][x], 0x5140);
-            const uint32_t r1_ = __byte_perm(vv[2][x], vv[3][x], 0x7362);
-            mma_f16(O[4 * x + 0], a, h2_of(p0), h2_of(r0_));
-            mma_f16(O[4 * x + 1], a, h2_of(p0 >> 16), h2_of(r0_ >> 16));
-            mma_f16(O[4 * x + 2], a, h2_of(p1), h2_of(r1_));
-            mma_f16(O[4 * x + 3], a, h2_of(p1 >> 16), h2_of(r1_ >> 16));
+            // bytes of the four values paired (key 0, key 1) and (key 2, key 3): bytes 0, 1 and
+            // 2, 3 of word x are dims 4x .. 4x+3 of this lane
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                h2x2_of(__byte_perm(vv[0][x], vv[1][x], y ? 0x7362 : 0x5140), a[0], a[1]);
+                h2x2_of(__byte_perm(vv[2][x], vv[3][x], y ? 0x7362 : 0x5140), a[2], a[3]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) mma_f16(O[2 * x + y][b], a, pb[b][0], pb[b][1]);
+            }
         }
     }
     cp_wait<0>();
 #pragma unroll
-    for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {     // the four lanes of a row hold parts of its sum
-        l[w] += __shfl_xor_sync(0xffffffffu, l[w], 1);
-        l[w] += __shfl_xor_sync(0xffffffffu, l[w], 2);
-    }
+    for (int b = 0; b < NS; ++b)            // the eight lanes of a column hold parts of its sum
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+                l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], o);
 
     // ---------------------------------------------------------------- join
-    // shared memory: warps' O [4][MT][D], m and l [4][MT]; this CTA's O [MT][D], m, l [MT]
+    // shared memory: warps' O [4][QT][D], m and l [4][QT]; this CTA's O [QT][D], m, l [QT]
     __syncthreads();
     float* wO = reinterpret_cast<float*>(smem);
-    float* wM = wO + kWarps * MT * D;
-    float* wL = wM + kWarps * MT;
-    float* cO = wL + kWarps * MT;
-    float* cM = cO + MT * D;
-    float* cL = cM + MT;
-    static_assert((kWarps + 1) * (MT * D + 2 * MT) * 4 <= ring_bytes<D>(), "join fits the ring");
-    {
-        float* o = wO + (warp * MT + g) * D;
+    float* wM = wO + kWarps * QT * D;
+    float* wL = wM + kWarps * QT;
+    float* cO = wL + kWarps * QT;
+    float* cM = cO + QT * D;
+    float* cL = cM + QT;
+    static_assert((kWarps + 1) * (QT * D + 2 * QT) * 4 <= ring_bytes<D>(), "join fits the ring");
+    if (MODE != PLAIN) {                    // leading and trailing parts
 #pragma unroll
-        for (int j = 0; j < VJ; ++j) {
-            // columns 2t, 2t+1 of product j: dims (2t) D/8 + j and (2t+1) D/8 + j
-            const int d0 = 2 * t * VJ + j, d1 = d0 + VJ;
-            if (SPLIT) {
-                o[d0] = fmaf(O[j][2], 1.f / 2048.f, O[j][0]);
-                o[d1] = fmaf(O[j][3], 1.f / 2048.f, O[j][1]);
-            } else {
-                o[d0] = O[j][0];
-                o[d1] = O[j][1];
-                o[8 * D + d0] = O[j][2];
-                o[8 * D + d1] = O[j][3];
-            }
-        }
-        if (t == 0) {
+        for (int j = 0; j < VJ; ++j)
 #pragma unroll
-            for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-                wM[warp * MT + g + 8 * w] = m[w];
-                wL[warp * MT + g + 8 * w] = l[w];
+            for (int i = 0; i < 4; ++i) {
+                const float rest =
+                    MODE == FOLD ? __shfl_xor_sync(0xffffffffu, O[j][0][i], 2) : O[j][NB - 1][i];
+                O[j][0][i] = fmaf(rest, 1.f / 2048.f, O[j][0][i]);
             }
-        }
     }
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * b + 2 * t + e;
+            if (r < live) {                 // FOLD: the lanes of columns 0-3
+                float* o = wO + (warp * QT + r) * D + g * (D / 8);
+#pragma unroll
+                for (int j = 0; j < VJ; ++j)
+                    *reinterpret_cast<float2*>(o + 2 * j) = make_float2(O[j][b][e], O[j][b][2 + e]);
+                if (g == 0) wM[warp * QT + r] = m[b][e], wL[warp * QT + r] = l[b][e];
+            }
+        }
     __syncthreads();
     auto put = [&](int r, int d, float o, float lsum) {
         const int rr = r0 + r;
-        if (rr < nq)
-            out.p[(int64_t)row * out.row + (int64_t)(rr / share) * out.token +
-                  (int64_t)(kvh * share + rr % share) * D + d] =
-                from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
+        out.p[(int64_t)row * out.row + (int64_t)(rr / share) * out.token +
+              (int64_t)(kvh * share + rr % share) * D + d] =
+            from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
     };
-    const int live = min(MT, nq - r0);
     for (int x = threadIdx.x; x < live * D; x += kWarps * 32) {
         const int r = x / D, d = x % D;
         float M = wM[r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wM[w * MT + r]);
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wM[w * QT + r]);
         float o = 0.f, ls = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float mw = wM[w * MT + r];
+            const float mw = wM[w * QT + r];
             const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-            o = fmaf(f, wO[(w * MT + r) * D + d], o);
-            ls = fmaf(f, wL[w * MT + r], ls);
+            o = fmaf(f, wO[(w * QT + r) * D + d], o);
+            ls = fmaf(f, wL[w * QT + r], ls);
         }
         if (nC == 1) {
             put(r, d, o, ls);
@@ -550,19 +619,18 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     cluster.sync();                         // no CTA leaves while its memory is read
 }
 
-template <int D, bool SPLIT, typename TQ, typename TO>
+template <int D, int MODE, int NB, typename TQ, typename TO>
 cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int heads, int n,
                 const int32_t* lens, int lens_add, float scale, const Rope8& rope,
                 cudaStream_t st) {
-    constexpr int MT = SPLIT ? 8 : 16;
-    auto* kern = k_cache8_attend<D, SPLIT, TQ, TO>;
+    constexpr int MT = queries_of(MODE, NB);
+    auto* kern = k_cache8_attend<D, MODE, NB, TQ, TO>;
     const void* kp = reinterpret_cast<const void*>(kern);
     const int share = heads / c.kv_heads, q_tiles = (n * share + MT - 1) / MT;
     int page_log2 = 4;
     while ((1 << page_log2) < c.page) ++page_log2;
     const int64_t cap = (int64_t)c.row_pages * c.page;
-    int C = 1;
-    while (C < kMaxCtas && (int64_t)C * kKeysPerCta < cap) C *= 2;
+    const int C = ctas_of(cap);
     const int64_t ctas = (int64_t)c.rows * c.kv_heads * q_tiles * C;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (!set_smem_once(kp, ring_bytes<D>()) || (C > 8 && !set_wide_cluster_once(kp)))
@@ -596,15 +664,16 @@ cudaError_t launch_cache8_attend(const Cache8& c, Tok8<const TQ> q, int slabs, s
                                  int lens_add, float scale, const Rope8& rope, cudaStream_t st) {
     if (c.rows <= 0 || n <= 0) return cudaSuccess;
     const QIn<TQ> qi{q.p, q.row, q.token, slabs, slab};
-    // 16-row tiles where the bf16 queries of a key head do not fit 8 rows
-    constexpr bool both16 = std::is_same<TQ, bf16>::value && std::is_same<TO, bf16>::value;
-    if constexpr (both16) {
-        if ((int64_t)n * (heads / c.kv_heads) > 8)
-            return c.dh == 64 ? run<64, false>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)
-                              : run<128, false>(c, qi, out, heads, n, lens, lens_add, scale, rope, st);
-    }
-    return c.dh == 64 ? run<64, true>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)
-                      : run<128, true>(c, qi, out, heads, n, lens, lens_add, scale, rope, st);
+    const int64_t nq = (int64_t)n * (heads / c.kv_heads);
+#define RLT_RUN(MODE, NB)                                                                       \
+    (c.dh == 64 ? run<64, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)       \
+                : run<128, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st))
+    if (nq <= 4) return RLT_RUN(FOLD, 1);
+    if constexpr (std::is_same<TQ, bf16>::value && std::is_same<TO, bf16>::value)
+        return nq <= 8 ? RLT_RUN(PLAIN, 1) : RLT_RUN(PLAIN, 2);
+    else
+        return RLT_RUN(SPLIT, 2);
+#undef RLT_RUN
 }
 
 #define RLT_INST(TQ, TO)                                                                         \

@@ -339,7 +339,9 @@ def test_attend(sd, case):
     torch.cuda.synchronize()
     assert int(cache.status) == 0
     assert bool((room[:, :, heads:] == 5.0).all())
-    _check_attend(cache, q, out, lens, scale, rope, t == "bf16" and n * heads // kv > 8)
+    # bf16 types and more than 4 queries to a key head: the weights w_j enter the product as fp16,
+    # each off by 2^-11 of itself at most, so sum w_j v_j / sum w_j moves by at most 2^-11 max |v|
+    _check_attend(cache, q, out, lens, scale, rope, t == "bf16" and n * heads // kv > 4)
     for b, L in enumerate(lens):
         for i in range(n):
             if L - n + i + 1 <= 0:
