@@ -115,7 +115,11 @@ __device__ __forceinline__ void fold_keys(Online<DH, NQ>& st, const float (&q)[N
 #pragma unroll
         for (int o = 16; o >= LPK; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
         const float mn = fmaxf(st.m[i], bm);
-        if (mn == -INFINITY) continue;
+        if (mn == -INFINITY) {                 // nothing seen yet: no weight, not -inf x v
+#pragma unroll
+            for (int rr = 0; rr < ROUNDS; ++rr) s[i][rr] = 0.f;
+            continue;
+        }
         const float corr = (st.m[i] == -INFINITY) ? 0.f : expf(st.m[i] - mn);
         float ps = 0.f;
 #pragma unroll
