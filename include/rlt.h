@@ -94,6 +94,21 @@ int rlt_model_config(const rlt_model* model, rlt_config* out);
 int rlt_state_create(rlt_model* model, int batch, int max_len, rlt_state** out);
 void rlt_state_destroy(rlt_state* state);
 
+/* rlt_state_create with flags (0: the same).  RLT_STATE_MEM8: the memory M is
+ * held in 8 bits, a paged cache as below (pages of 64 positions, one scale per
+ * page, head and K or V): about half the bytes of bf16 to hold and to stream
+ * through every transition's cross-attention.  Keys and values go to it from
+ * the fp32 products, rotated first, rounded once.  Everything else is held as
+ * before.  Such a state's results differ from a plain one's by the rounding of
+ * M, and in the last bits with how a prompt is split over rlt_encode calls (a
+ * page whose scale grows rounds its smallest values again).  RLT_E_UNSUPPORTED
+ * for a head size other than 64 and 128; rlt_state_save and rlt_state_load
+ * return RLT_E_UNSUPPORTED (a snapshot carries M in the model dtype).
+ * RLT_E_ARG for an unknown flag. */
+#define RLT_STATE_MEM8 1u
+int rlt_state_create_with(rlt_model* model, int batch, int max_len, uint32_t flags,
+                          rlt_state** out);
+
 /* Bytes of the per-row state proper (eq. 3.3 terms) and of everything the
  * state allocated on the device (state + scratch). */
 int rlt_state_bytes(const rlt_state* state, size_t* per_row_state, size_t* total_device);
@@ -222,6 +237,9 @@ int rlt_state_positions(const rlt_state* state, int32_t* pos_enc, int32_t* pos_d
  * RLT_PART_S / _R: fp32 [batch][d]; _E: fp32 [batch][max_len][d];
  * _MEM: model dtype [batch][G][2][h][max_len][d_h]; _RING: model dtype
  * [batch][L_D][2][h][W-1][d_h]; _ENC: model dtype [batch][L_E][2][h][max_len][d_h].
+ * In a RLT_STATE_MEM8 state _MEM is e4m3 [G][batch * P][2][h][64][d_h], P =
+ * ceil(max_len / 64), row b's positions 64 j + 1 .. in page b P + j, and
+ * _MEM_SCALES fp32 [G][batch * P][2][h] (RLT_E_UNSUPPORTED in other states).
  * Synchronises `stream` when dst is host memory. */
 #define RLT_PART_S    0
 #define RLT_PART_R    1
@@ -229,6 +247,7 @@ int rlt_state_positions(const rlt_state* state, int32_t* pos_enc, int32_t* pos_d
 #define RLT_PART_MEM  3
 #define RLT_PART_RING 4
 #define RLT_PART_ENC  5
+#define RLT_PART_MEM_SCALES 6
 int rlt_state_read(rlt_state* state, int part, void* dst, size_t nbytes, size_t* nbytes_out,
                    void* stream);
 
@@ -441,6 +460,35 @@ int rlt_beam_select(int dtype, const void* logits, const float* scores, const ui
 int rlt_rows_reorder(void* rows, const int32_t* parents, int groups, int beams, int64_t row_stride,
                      int planes, int64_t plane_stride, int64_t offset, int64_t bytes,
                      void* stream);
+
+/* Beam search over the rows of a state: rows g*beams .. g*beams + beams - 1 are
+ * the beams of search g (beams divides batch, at most 64; RLT_E_ARG) and stand
+ * at equal positions (else RLT_E_ORDER).
+ *
+ * rlt_state_reorder: row g*beams + i takes up all that row g*beams +
+ * parents[g*beams + i] needs to continue (s, R, the window rings, C^E, M, the
+ * e_t not yet consumed), all rows at once, in place.  The rows of a search
+ * hold the same C^E and M at positions 1 .. shared (a common prompt; 0: none
+ * promised), which are not moved.  parents: int32 [batch], host or device; on
+ * the host an entry outside [0, beams) is RLT_E_ARG, on the device it leaves
+ * its row as it was.  e_t of consumed positions stay where they are. */
+int rlt_state_reorder(rlt_state* state, const int32_t* parents, int beams, int shared,
+                      void* stream);
+
+/* One step of beam search: the readout of every row, rlt_beam_select with k =
+ * beams over logits / temperature, rlt_state_reorder by the chosen parents,
+ * then the chosen tokens are encoded and consumed (one transition).  scores
+ * (fp32 [batch], log-probabilities so far) and finished (uint8 [batch], may be
+ * NULL: no beam ends) are read and replaced; parents (within the search) and
+ * tokens (int32 [batch]) receive what was chosen: the caller keeps them, step
+ * by step, to read the sequences back.  A finished beam goes on with eos at an
+ * unchanged score.  A search starts with all rows past the prompt, scores 0
+ * for its first row and -infinity for the others.  All four arrays are device
+ * memory.  The first call allocates 5 * batch bytes in the state.  RLT_E_ORDER
+ * when a row has encoded tokens not yet consumed, RLT_E_CAPACITY at max_len;
+ * argument limits as rlt_beam_select's. */
+int rlt_beam_step(rlt_state* state, float* scores, uint8_t* finished, int eos, float temperature,
+                  int beams, int shared, int32_t* parents, int32_t* tokens, void* stream);
 
 /* Number of kernels this library has launched in this process. */
 uint64_t rlt_kernel_launches(void);

@@ -35,7 +35,8 @@ RLT_E_BLOB, RLT_E_DEVICE, RLT_E_TIMEOUT, RLT_E_UNSUPPORTED = -5, -6, -7, -8
 RLT_E_SNAPSHOT = -9
 RLT_BUILD_DEBUG = 1
 SNAPSHOT_HEADER_BYTES = 128                # RLT_SNAPSHOT_HEADER_BYTES
-PART_S, PART_R, PART_E, PART_MEM, PART_RING, PART_ENC = range(6)
+PART_S, PART_R, PART_E, PART_MEM, PART_RING, PART_ENC, PART_MEM_SCALES = range(7)
+STATE_MEM8 = 1
 PROF_XATTN, PROF_SWA, PROF_STEP, PROF_ENC, PROF_ENC1 = range(5)
 PROF_NCLS = 5          # cls + PROF_NCLS * (layer + 1): one decoder layer's launches
 READOUT_ROWS_SCRATCH_BYTES = 16 << 20      # RLT_READOUT_ROWS_SCRATCH_BYTES
@@ -67,6 +68,9 @@ _SIGS = {
                                _vp]),
     "rlt_beam_select": (_i, [_i, _vp, _vp, _vp, _i, _f32, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                              _vp]),
+    "rlt_state_create_with": (_i, [_vp, _i, _i, ctypes.c_uint32, ctypes.POINTER(_vp)]),
+    "rlt_state_reorder": (_i, [_vp, _vp, _i, _i, _vp]),
+    "rlt_beam_step": (_i, [_vp, _vp, _vp, _i, _f32, _i, _i, _vp, _vp, _vp]),
     "rlt_rows_reorder": (_i, [_vp, _vp, _i, _i, _i64, _i, _i64, _i64, _i64, _vp]),
     "rlt_create": (_i, [_vp, _sz, _i, ctypes.POINTER(_vp)]),
     "rlt_destroy": (None, [_vp]),
@@ -197,6 +201,22 @@ def rlt_state_create(model, batch: int, max_len: int):
     h = _vp()
     code = _lib.rlt_state_create(model, batch, max_len, ctypes.byref(h))
     return code, h.value
+
+
+def rlt_state_create_with(model, batch: int, max_len: int, flags: int = 0):
+    out = _vp()
+    code = _lib.rlt_state_create_with(model, batch, max_len, flags, ctypes.byref(out))
+    return code, out.value
+
+
+def rlt_state_reorder(state, parents, beams: int, shared: int = 0, stream=None) -> int:
+    return _lib.rlt_state_reorder(state, _ptr(parents), beams, shared, _stream(stream))
+
+
+def rlt_beam_step(state, scores, finished, eos: int, temperature: float, beams: int, shared: int,
+                  parents, tokens, stream=None) -> int:
+    return _lib.rlt_beam_step(state, _ptr(scores), _ptr(finished), eos, temperature, beams, shared,
+                              _ptr(parents), _ptr(tokens), _stream(stream))
 
 
 def rlt_state_destroy(state) -> None:
@@ -332,21 +352,41 @@ DTYPE_F32, DTYPE_BF16 = 0, 1               # RLT_DTYPE_*
 _DTYPES = {"float32": DTYPE_F32, "bfloat16": DTYPE_BF16}
 
 
+_dtype_names = {}                          # of the element types met so far
+
+
+def _dtype_name(x) -> str:
+    dt = x.dtype
+    name = _dtype_names.get(dt)
+    if name is None:
+        name = _dtype_names[dt] = str(dt).replace("torch.", "")
+    return name
+
+
 def _device_buf(x, what: str, dtypes, shape=None, device=None):
     """Address of a CUDA tensor after its type, shape (None: any extent) and
-    device are checked; strides are the caller's to check."""
+    device (an index) are checked; strides are the caller's to check.  The
+    calls below are a few microseconds long, so what is right passes in one
+    comparison each."""
+    try:
+        at = x.get_device()
+        if at >= 0 and (at == device or device is None) and _dtype_name(x) in dtypes and \
+                (shape is None or x.shape == shape):
+            return x.data_ptr()
+    except AttributeError:
+        pass
     if not getattr(x, "is_cuda", False):
         raise TypeError(f"{what}: expected a CUDA tensor, got {type(x).__name__}"
                         f"{' on the host' if hasattr(x, 'data_ptr') else ''}")
-    name = str(x.dtype).replace("torch.", "")
+    name = _dtype_name(x)
     if name not in dtypes:
         raise TypeError(f"{what}: element type {name}, expected {' or '.join(dtypes)}")
     if shape is not None and (len(x.shape) != len(shape) or
                               any(b is not None and a != b for a, b in zip(x.shape, shape))):
         raise ValueError(f"{what}: shape {tuple(x.shape)}, expected "
                          f"({', '.join('*' if b is None else str(b) for b in shape)})")
-    if device is not None and x.device != device:
-        raise ValueError(f"{what}: on {x.device}, expected {device}")
+    if device is not None and x.get_device() != device:
+        raise ValueError(f"{what}: on {x.device}, expected cuda:{device}")
     return x.data_ptr()
 
 
@@ -375,10 +415,11 @@ class Rope:
     def __init__(self, cos, sin, interleaved: bool = False, origin: int = 0):
         positions, half = (int(n) for n in cos.shape)
         self.buffers = (cos, sin)
-        self.device = cos.device
-        self.struct = rlt_rope(_dense(cos, "cos", ("float32",)),
-                               _dense(sin, "sin", ("float32",), (positions, half), cos.device),
+        p = _dense(cos, "cos", ("float32",))
+        self.device = cos.get_device()
+        self.struct = rlt_rope(p, _dense(sin, "sin", ("float32",), (positions, half), self.device),
                                positions, 2 * half, int(bool(interleaved)), origin)
+        self._ref = ctypes.byref(self.struct)
 
 
 class Cache8:
@@ -390,7 +431,7 @@ class Cache8:
     def __init__(self, pages, scales, table, status=None):
         p = _dense(pages, "pages", ("uint8", "float8_e4m3fn"), (None, 2, None, None, None))
         n_pages, _, kv_heads, page, dh = (int(n) for n in pages.shape)
-        self.device = pages.device
+        self.device = pages.get_device()
         s = _dense(scales, "scales", ("float32",), (n_pages, 2, kv_heads), self.device)
         t = _dense(table, "table", ("int32",), (None, None), self.device)
         w = None if status is None else _dense(status, "status", ("int32",), (1,), self.device)
@@ -404,17 +445,18 @@ class Cache8:
         if rope is None:
             return None
         if rope.device != self.device:
-            raise ValueError(f"rope: on {rope.device}, expected {self.device}")
-        return ctypes.byref(rope.struct)
+            raise ValueError(f"rope: on cuda:{rope.device}, expected cuda:{self.device}")
+        return rope._ref
 
     def append(self, k, v, start, counts=None, rope: Optional[Rope] = None, stream=None):
         """Append k, v ([rows][n][kv_heads][dh] fp32 or bf16; row and token strides are free) at
         tokens start[b] .. start[b]+counts[b]-1 (int32 [rows]; counts None: n each), k rotated
         first when rope is given."""
-        n = int(k.shape[1]) if len(k.shape) == 4 else 0
+        ks = k.shape
+        n = ks[1] if len(ks) == 4 else 0
         shape = (self.rows, n, self.kv_heads, self.dh)
         kp, kr, kt = _heads_tensor(k, "k", _DTYPES, shape, self.device)
-        name = str(k.dtype).replace("torch.", "")
+        name = _dtype_name(k)
         vp, vr, vt = _heads_tensor(v, "v", (name,), shape, self.device)
         sp = _dense(start, "start", ("int32",), (self.rows,), self.device)
         cp = None if counts is None else _dense(counts, "counts", ("int32",), (self.rows,),
@@ -427,10 +469,11 @@ class Cache8:
                stream=None):
         """out = attention of q ([rows][n][heads][dh]) over each row's first lens[b] tokens, query i
         seeing tokens 0 .. lens[b] - n + i; scale defaults to 1/sqrt(dh)."""
-        n, heads = (int(q.shape[1]), int(q.shape[2])) if len(q.shape) == 4 else (0, 0)
+        qs = q.shape
+        n, heads = (qs[1], qs[2]) if len(qs) == 4 else (0, 0)
         shape = (self.rows, n, heads, self.dh)
         qp, qr, qt = _heads_tensor(q, "q", _DTYPES, shape, self.device)
-        name = str(q.dtype).replace("torch.", "")
+        name = _dtype_name(q)
         op, o_r, ot = _heads_tensor(out, "out", (name,), shape, self.device)
         lp = _dense(lens, "lens", ("int32",), (self.rows,), self.device)
         if scale is None:
@@ -446,19 +489,19 @@ def beam_select(logits, scores, parents, tokens, new_scores, finished=None, new_
     [groups][beams][vocab], scores fp32 [groups][beams], finished uint8 [groups][beams]; outputs
     parents and tokens int32, new_scores fp32, new_finished uint8, each [groups][k]."""
     lp = _dense(logits, "logits", _DTYPES, (None, None, None))
-    groups, beams, vocab = (int(n) for n in logits.shape)
-    dev = logits.device
-    pp = _dense(parents, "parents", ("int32",), (groups, None), dev)
-    k = int(parents.shape[1])
-    opt = lambda x, what, shape: None if x is None else _dense(  # noqa: E731
-        x, what, ("uint8",), shape, dev)
+    groups, beams, vocab = logits.shape
+    dev = logits.get_device()
+    ps = parents.shape if len(getattr(parents, "shape", ())) == 2 else (groups, None)
+    k = ps[1]
+    out, per = (groups, k), (groups, beams)
+    pp = _dense(parents, "parents", ("int32",), out, dev)
     return _check(_lib.rlt_beam_select(
-        _DTYPES[str(logits.dtype).replace("torch.", "")], lp,
-        _dense(scores, "scores", ("float32",), (groups, beams), dev),
-        opt(finished, "finished", (groups, beams)), eos, temperature, groups, beams, vocab, k, pp,
-        _dense(tokens, "tokens", ("int32",), (groups, k), dev),
-        _dense(new_scores, "new_scores", ("float32",), (groups, k), dev),
-        opt(new_finished, "new_finished", (groups, k)), _stream(stream)), "rlt_beam_select")
+        _DTYPES[_dtype_name(logits)], lp, _dense(scores, "scores", ("float32",), per, dev),
+        None if finished is None else _dense(finished, "finished", ("uint8",), per, dev), eos,
+        temperature, groups, beams, vocab, k, pp, _dense(tokens, "tokens", ("int32",), out, dev),
+        _dense(new_scores, "new_scores", ("float32",), out, dev),
+        None if new_finished is None else _dense(new_finished, "new_finished", ("uint8",), out, dev),
+        _stream(stream)), "rlt_beam_select")
 
 
 def rows_reorder(rows, parents, start: int = 0, stop: Optional[int] = None, stream=None):
@@ -467,14 +510,15 @@ def rows_reorder(rows, parents, start: int = 0, stop: Optional[int] = None, stre
     [groups][beams]; positions [start, stop) of every plane of row g*beams + i take what row
     g*beams + parents[g][i] held."""
     pp = _dense(parents, "parents", ("int32",), (None, None))
-    groups, beams = (int(n) for n in parents.shape)
+    groups, beams = parents.shape
     if not getattr(rows, "is_cuda", False):
         raise TypeError("rows: expected a CUDA tensor")
-    if rows.device != parents.device:
+    if rows.get_device() != parents.get_device():
         raise ValueError(f"rows: on {rows.device}, expected {parents.device}")
-    if len(rows.shape) != 4 or int(rows.shape[0]) != groups * beams:
-        raise ValueError(f"rows: shape {tuple(rows.shape)}, expected ({groups * beams}, *, *, *)")
-    _, planes, cap, width = (int(n) for n in rows.shape)
+    shape = rows.shape
+    if len(shape) != 4 or shape[0] != groups * beams:
+        raise ValueError(f"rows: shape {tuple(shape)}, expected ({groups * beams}, *, *, *)")
+    _, planes, cap, width = shape
     stop = cap if stop is None else stop
     if not 0 <= start <= stop <= cap:
         raise ValueError(f"rows: positions [{start}, {stop}) of {cap}")
@@ -532,11 +576,13 @@ class Model:
 
 
 class State:
-    def __init__(self, model: Model, batch: int, max_len: int):
+    def __init__(self, model: Model, batch: int, max_len: int, mem8: bool = False):
+        """mem8: the memory M is held as e4m3 pages (RLT_STATE_MEM8)."""
         self.model = model
         self.batch, self.max_len = batch, max_len
-        code, self.handle = rlt_state_create(model.handle, batch, max_len)
-        _check(code, "rlt_state_create")
+        code, self.handle = rlt_state_create_with(model.handle, batch, max_len,
+                                                  STATE_MEM8 if mem8 else 0)
+        _check(code, "rlt_state_create_with" if mem8 else "rlt_state_create")
 
     def close(self):
         if self.handle:
@@ -577,6 +623,25 @@ class State:
         _check_buf(sampled, "int32", "sampled", self.batch)
         return _check(rlt_readout(self.handle, logits, argmax, sampled, seed, step, temperature,
                                   stream), "rlt_readout")
+
+    def reorder(self, parents, beams: int, shared: int = 0, stream=None):
+        """Rows g*beams + i take up rows g*beams + parents[g*beams + i] (int32 [batch], host or
+        CUDA), caches from position `shared` on."""
+        _check_buf(parents, "int32", "parents", self.batch)
+        return _check(rlt_state_reorder(self.handle, parents, beams, shared, stream),
+                      "rlt_state_reorder")
+
+    def beam_step(self, scores, parents, tokens, beams: int, finished=None, eos: int = -1,
+                  temperature: float = 1.0, shared: int = 0, stream=None):
+        """One step of beam search over groups of `beams` rows (rlt_beam_step): CUDA tensors
+        scores fp32 and finished uint8 [batch], read and replaced, and parents and tokens int32
+        [batch], written."""
+        _check_buf(scores, "float32", "scores", self.batch)
+        _check_buf(finished, "uint8", "finished", self.batch)
+        _check_buf(parents, "int32", "parents", self.batch)
+        _check_buf(tokens, "int32", "tokens", self.batch)
+        return _check(rlt_beam_step(self.handle, scores, finished, eos, temperature, beams, shared,
+                                    parents, tokens, stream), "rlt_beam_step")
 
     def replay_logprobs(self, tokens, logprobs=None, temperature=1.0, stream=None):
         """log p of each given token (int32 [batch][n]) read before it is

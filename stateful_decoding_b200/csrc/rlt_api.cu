@@ -23,6 +23,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/rlt.h"
+#include "beam.cuh"
+#include "cache8.cuh"
 #include "kernels.cuh"
 
 // An NVTX range over each public call, so that a profiler's timeline shows
@@ -519,6 +521,15 @@ struct rlt_state {
     float* P = nullptr;             // split-K partial slabs of the transition's projections
     size_t p_cols = 0;              // columns of one slab row (the widest projection)
     int p_slabs = 1;                // slabs allocated
+    // RLT_STATE_MEM8: `mem` holds e4m3 pages instead, [G][B * mem8_pages][2][h][kMem8Page][dh], with
+    // their scales [G][B * mem8_pages][2][h]; row b's page j is b * mem8_pages + j
+    bool mem8 = false;
+    int mem8_pages = 0;             // pages of one row
+    float* mem8_scales = nullptr;
+    int32_t* mem8_table = nullptr;
+    // rlt_beam_step: new scores and finished flags, allocated on first use
+    float* beam_scores = nullptr;
+    uint8_t* beam_fin = nullptr;
     std::vector<void*> allocs;
     size_t bytes = 0;
     // live timing (rlt_profile_*)
@@ -641,9 +652,21 @@ static size_t max_rows_per_call() {
     return (size_t)std::max(256L, x);
 }
 
+// Tokens of a page of the 8-bit memory: pages are what a reordering moves at
+// least and share one scale; 64 keys of one head are 4-8 KB, a run of whole
+// tiles of the attention.
+static constexpr int kMem8Page = 64;
+
 extern "C" int rlt_state_create(rlt_model* m, int batch, int max_len, rlt_state** out) {
-    if (!m || !out || batch <= 0 || max_len <= 0) return RLT_E_ARG;
+    return rlt_state_create_with(m, batch, max_len, 0, out);
+}
+
+extern "C" int rlt_state_create_with(rlt_model* m, int batch, int max_len, uint32_t flags,
+                                     rlt_state** out) {
+    if (!m || !out || batch <= 0 || max_len <= 0 || (flags & ~RLT_STATE_MEM8)) return RLT_E_ARG;
     *out = nullptr;
+    const bool mem8 = flags & RLT_STATE_MEM8;
+    if (mem8 && m->dh != 64 && m->dh != 128) return RLT_E_UNSUPPORTED;
     if (cudaSetDevice(m->device) != cudaSuccess) return RLT_E_DEVICE;
     const rlt_config& c = m->cfg;
     {   // every allocation below (caches, rings, scratch, split-K slabs,
@@ -667,7 +690,15 @@ extern "C" int rlt_state_create(rlt_model* m, int batch, int max_len, rlt_state*
     s->n_dec_blk = c.variant == 2 ? c.chunk : (c.variant == 0 ? std::min(s->n_enc_blk, 16) : 1);
     const size_t R = B * (size_t)std::max(s->n_enc_blk, s->n_dec_blk);
     s->enc_row = (size_t)c.n_enc * 2 * h * T * dh;
-    s->mem_row = (size_t)(c.n_dec > 0 ? c.groups : 0) * 2 * h * T * dh;
+    const size_t G = c.n_dec > 0 ? c.groups : 0;
+    s->mem_row = G * 2 * h * T * dh;
+    s->mem8 = mem8;
+    s->mem8_pages = mem8 ? (int)((T + kMem8Page - 1) / kMem8Page) : 0;
+    const size_t n_pages = B * (size_t)s->mem8_pages, page8 = 2 * h * kMem8Page * dh;
+    if (mem8 && n_pages > 0x7fffffff) {
+        delete s;
+        return RLT_E_OOM;
+    }
     s->ring_row = (size_t)c.n_dec * 2 * h * slots * dh;
     int rc = RLT_OK;
     auto take = [&](void** p, size_t bytes) {
@@ -678,7 +709,11 @@ extern "C" int rlt_state_create(rlt_model* m, int batch, int max_len, rlt_state*
     take((void**)&s->Rr, B * d * 4);
     take((void**)&s->e, B * T * d * 4);
     take(&s->enc, B * s->enc_row * elt);
-    take(&s->mem, B * s->mem_row * elt);
+    take(&s->mem, mem8 ? G * n_pages * page8 : B * s->mem_row * elt);
+    if (mem8) {
+        take((void**)&s->mem8_scales, G * n_pages * 2 * h * 4);
+        take((void**)&s->mem8_table, n_pages * 4);
+    }
     take(&s->ring, B * s->ring_row * elt);
     take((void**)&s->pos_enc, B * 4);
     take((void**)&s->pos_dec, B * 4);
@@ -721,6 +756,13 @@ extern "C" int rlt_state_create(rlt_model* m, int batch, int max_len, rlt_state*
     cudaError_t e1 = cudaMemcpy(s->rope_cs, cs.data(), cs.size() * 4, cudaMemcpyHostToDevice);
     cudaError_t e2 = cudaMemcpy(s->rope_sn, sn.data(), sn.size() * 4, cudaMemcpyHostToDevice);
     cudaError_t e3 = cudaMemset(s->err, 0, 4);
+    if (mem8 && !e3) {                       // every page in its place; bytes and scales defined
+        std::vector<int32_t> table(n_pages);
+        for (size_t i = 0; i < n_pages; ++i) table[i] = (int32_t)i;
+        e3 = cudaMemcpy(s->mem8_table, table.data(), n_pages * 4, cudaMemcpyHostToDevice);
+        if (!e3) e3 = cudaMemset(s->mem, 0, G * n_pages * page8);
+        if (!e3) e3 = cudaMemset(s->mem8_scales, 0, G * n_pages * 2 * h * 4);
+    }
     if (e1 || e2 || e3) {
         rlt_state_destroy(s);
         return RLT_E_DEVICE;
@@ -740,8 +782,11 @@ extern "C" int rlt_state_create(rlt_model* m, int batch, int max_len, rlt_state*
 extern "C" int rlt_state_bytes(const rlt_state* s, size_t* per_row_state, size_t* total) {
     if (!s) return RLT_E_ARG;
     const rlt_config& c = s->m->cfg;
+    const size_t G = c.n_dec > 0 ? c.groups : 0;
+    const size_t mem = s->mem8 ? G * s->mem8_pages * 2 * c.heads * ((size_t)kMem8Page * s->m->dh + 4)
+                               : s->mem_row * s->m->elt;
     if (per_row_state)
-        *per_row_state = (s->enc_row + s->mem_row + s->ring_row) * s->m->elt + (size_t)c.d * 4;
+        *per_row_state = (s->enc_row + s->ring_row) * s->m->elt + mem + (size_t)c.d * 4;
     if (total) *total = s->bytes;
     return RLT_OK;
 }
@@ -772,13 +817,17 @@ static rlt::RopeTab rope_of(rlt_state* s) {
 // weights excluded unless they cannot stay on chip)
 // ============================================================================
 static double kv_bytes(const rlt_state* s) { return 2.0 * s->m->cfg.d * (double)s->m->elt; }
+// of one position of the memory (8-bit: bytes and the position's part of its page's scales)
+static double mem_bytes(const rlt_state* s) {
+    return s->mem8 ? 2.0 * s->m->cfg.d + 8.0 * s->m->cfg.heads / kMem8Page : kv_bytes(s);
+}
 
 // (rows b0 .. b0+nb-1; all rows by default)
 static double xattn_bytes(const rlt_state* s, int n, int b0 = 0, int nb = -1) {
     const double d = s->m->cfg.d, elt = (double)s->m->elt;
     double by = 0;
     for (int b = b0; b < (nb < 0 ? s->B : b0 + nb); ++b)
-        by += (s->h_pos_dec[b] + n) * kv_bytes(s) + n * (d * 4 + d * elt);
+        by += (s->h_pos_dec[b] + n) * mem_bytes(s) + n * (d * 4 + d * elt);
     return by;
 }
 static double swa_bytes(const rlt_state* s, int n, int b0 = 0, int nb = -1) {
@@ -799,7 +848,7 @@ static double step_bytes(const rlt_state* s, int n) {    // one whole transition
     double by = 0;
     for (int b = 0; b < s->B; ++b) {
         const int pd = s->h_pos_dec[b];
-        by += c.n_dec * ((pd + n) * kv_bytes(s) + std::min(pd, slots) * kv_bytes(s) +
+        by += c.n_dec * ((pd + n) * mem_bytes(s) + std::min(pd, slots) * kv_bytes(s) +
                          std::min(n, slots) * kv_bytes(s));
         by += n * c.d * 4.0 + 2.0 * c.d * 4.0;            // e_t in, s in and out
     }
@@ -813,7 +862,7 @@ static double enc_bytes(const rlt_state* s, int n) {     // one encoder block
     for (int b = 0; b < s->B; ++b) {
         const int p0 = s->h_pos_enc[b];
         // cache and memory written for n positions; cached keys/values re-read
-        by += (c.n_enc + (c.n_dec ? c.groups : 0)) * n * kv_bytes(s) +
+        by += n * (c.n_enc * kv_bytes(s) + (c.n_dec ? c.groups : 0) * mem_bytes(s)) +
               c.n_enc * (double)p0 * kv_bytes(s) + n * (4.0 + c.d * 4.0);
     }
     return by;
@@ -847,6 +896,20 @@ static int max_dec_splits(const rlt_config& c, int fp) {
     int m = 1;
     for (auto& sh : shapes) m = std::max(m, dec_splits_for(c, sh[0], sh[1]));
     return m;
+}
+
+// group g's 8-bit memory of the rows from b0 on
+static rlt::Cache8 mem8_of(const rlt_state* s, int g, int b0, int rows) {
+    const rlt_config& c = s->m->cfg;
+    const size_t n_pages = (size_t)s->B * s->mem8_pages;
+    return {(uint8_t*)s->mem + (size_t)g * n_pages * 2 * c.heads * kMem8Page * s->m->dh,
+            s->mem8_scales + (size_t)g * n_pages * 2 * c.heads,
+            s->mem8_table + (size_t)b0 * s->mem8_pages, s->err, rlt::kDevBounds, rlt::kDevCapacity,
+            (int)n_pages, rows, s->mem8_pages, kMem8Page, c.heads, s->m->dh};
+}
+// positions are 1-based: token j of a row is position j + 1
+static rlt::Rope8 mem8_rope(const rlt_state* s) {
+    return {s->rope_cs, s->rope_sn, s->T_cap + 1, s->m->dh, 0, 1};
 }
 
 // ============================================================================
@@ -926,6 +989,15 @@ static void encode_block(rlt_state* s, const int32_t* tok, int n, cudaStream_t s
         for (int g = 0; g < c.groups; ++g) {
             T* mem_g = (T*)s->mem + g * layer_mem;
             bool kv_done = false;
+            if (s->mem8) {                   // from the product in fp32: rotated and rounded once
+                launch_gemm<T>(Y, d, (const T*)m->wmem[g], d, s->QKV, 2 * d, nullptr, 0, R,
+                               2 * d, d, kStoreF32, st);
+                launch_cache8_append<float>(mem8_of(s, g, 0, B),
+                                            {s->QKV, (int64_t)n * 2 * d, 2 * d},
+                                            {s->QKV + d, (int64_t)n * 2 * d, 2 * d}, s->pos_enc,
+                                            nullptr, n, mem8_rope(s), st);
+                continue;
+            }
             if constexpr (std::is_same<T, bf16>::value)
                 kv_done = launch_gemm_rope_scatter(
                     Y, d, (const bf16*)m->wmem[g], d, R, 2 * d, d,
@@ -1070,8 +1142,13 @@ static void step_block(rlt_state* s, int n, cudaStream_t st, bool merged_in = fa
             (const T*)s->mem + (size_t)b0 * s->mem_row + (c.groups > 1 ? l : 0) * layer_mem;
         {
             ProfScope ps(s, RLT_PROF_XATTN, st, s->prof ? xattn_bytes(s, n, b0, B) : 0.0, l);
-            bool done = false;
-            if constexpr (std::is_same<T, bf16>::value)
+            bool done = s->mem8;
+            if (done)
+                launch_cache8_attend<float, T>(mem8_of(s, c.groups > 1 ? l : 0, b0, B),
+                                               {P, (int64_t)n * d, d}, np, slab,
+                                               {A, (int64_t)n * d, d}, h, n, pos_dec, n,
+                                               1.f / sqrtf((float)dh), mem8_rope(s), st);
+            else if constexpr (std::is_same<T, bf16>::value)
                 done = launch_attn_cross_proj(ProjIn{P, np, slab, d, rope_of(s)}, mem, s->mem_row,
                                               s->T_cap, pos_dec, A, B, n, h, dh, st);
             if (!done) {
@@ -1518,6 +1595,120 @@ extern "C" int rlt_prefill_packed(rlt_state* s, const int32_t* tokens, const uin
 }
 
 // ============================================================================
+// beam search: rows of one search, forked and dropped as its beams are
+// ============================================================================
+// groups of `beams` rows at one position each
+static int check_groups(const rlt_state* s, int beams) {
+    if (beams < 1 || beams > rlt::kMaxBeams || s->B % beams) return RLT_E_ARG;
+    for (int b = 0; b < s->B; ++b) {
+        const int lead = b / beams * beams;
+        if (s->h_pos_enc[b] != s->h_pos_enc[lead] || s->h_pos_dec[b] != s->h_pos_dec[lead])
+            return RLT_E_ORDER;
+    }
+    return RLT_OK;
+}
+
+// every row takes up row parents[row] of its group: all that it needs to continue, the caches from
+// position `shared` on
+static int reorder_rows(rlt_state* s, const int32_t* parents, int beams, int shared,
+                        cudaStream_t st) {
+    const rlt_config& c = s->m->cfg;
+    const int64_t d = c.d, dh = s->m->dh, elt = s->m->elt, T = s->T_cap;
+    int longest = 0, consumed = T;
+    for (int b = 0; b < s->B; ++b) {
+        longest = std::max(longest, s->h_pos_enc[b]);
+        consumed = std::min(consumed, s->h_pos_dec[b]);
+    }
+    rlt::ReorderSeg seg[rlt::kMaxSegs];
+    int n = 0;
+    seg[n++] = {(uint8_t*)s->s, d * 4, 0, d * 4, nullptr, 0, 1, 1, 1};
+    if (c.variant == 2) seg[n++] = {(uint8_t*)s->Rr, d * 4, 0, d * 4, nullptr, 0, 1, 1, 1};
+    const int64_t ring = (int64_t)s->ring_row * elt;
+    seg[n++] = {(uint8_t*)s->ring, ring, 0, ring, nullptr, 0, 1, 1, 1};
+    // e_t of the positions that transitions still have to merge
+    seg[n++] = {(uint8_t*)s->e, T * d * 4, 0, d * 4, s->pos_enc, consumed, longest, 1, 1};
+    seg[n++] = {(uint8_t*)s->enc, (int64_t)s->enc_row * elt, T * dh * elt, dh * elt, s->pos_enc,
+                shared, longest, 2 * c.n_enc * c.heads, 1};
+    if (c.n_dec > 0 && !s->mem8) {
+        seg[n++] = {(uint8_t*)s->mem, (int64_t)s->mem_row * elt, T * dh * elt, dh * elt,
+                    s->pos_enc, shared, longest, 2 * c.groups * c.heads, 1};
+    } else if (c.n_dec > 0) {
+        const int64_t page = 2 * c.heads * kMem8Page * dh, row = s->mem8_pages * page;
+        seg[n++] = {(uint8_t*)s->mem, row, s->B * row, page, s->pos_enc, shared, longest,
+                    c.groups, kMem8Page};
+        const int64_t sc = 2 * c.heads * 4, srow = s->mem8_pages * sc;
+        seg[n++] = {(uint8_t*)s->mem8_scales, srow, s->B * srow, sc, s->pos_enc, shared, longest,
+                    c.groups, kMem8Page};
+    }
+    const cudaError_t e = rlt::launch_reorder(seg, n, parents, s->B / beams, beams, st);
+    if (e == cudaSuccess) return RLT_OK;
+    cudaGetLastError();
+    return e == cudaErrorInvalidConfiguration ? RLT_E_UNSUPPORTED : RLT_E_DEVICE;
+}
+
+extern "C" int rlt_state_reorder(rlt_state* s, const int32_t* parents, int beams, int shared,
+                                 void* stream) {
+    NvtxRange nvtx("rlt_state_reorder");
+    if (!s || !parents || shared < 0) return RLT_E_ARG;
+    if (int rc = check_groups(s, beams)) return rc;
+    if (cudaSetDevice(s->m->device) != cudaSuccess) return RLT_E_DEVICE;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const int32_t* p = parents;
+    if (!is_device_ptr(parents)) {
+        for (int b = 0; b < s->B; ++b)
+            if (parents[b] < 0 || parents[b] >= beams) return RLT_E_ARG;
+        if (cudaMemcpyAsync(s->rows, parents, (size_t)s->B * 4, cudaMemcpyHostToDevice, st) ||
+            cudaStreamSynchronize(st))      // the caller may reuse its array
+            return RLT_E_DEVICE;
+        p = s->rows;
+    }
+    return reorder_rows(s, p, beams, shared, st);
+}
+
+extern "C" int rlt_beam_step(rlt_state* s, float* scores, uint8_t* finished, int eos,
+                             float temperature, int beams, int shared, int32_t* parents,
+                             int32_t* tokens, void* stream) {
+    NvtxRange nvtx("rlt_beam_step");
+    if (!s || !scores || !parents || !tokens || shared < 0) return RLT_E_ARG;
+    const rlt_config& c = s->m->cfg;
+    if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f) || eos >= c.vocab ||
+        (finished && eos < 0) || c.vocab >= (1 << 24))
+        return RLT_E_ARG;
+    if (int rc = check_groups(s, beams)) return rc;
+    for (int b = 0; b < s->B; ++b) {
+        if (s->h_pos_dec[b] != s->h_pos_enc[b]) return RLT_E_ORDER;
+        if (s->h_pos_enc[b] >= s->T_cap) return RLT_E_CAPACITY;
+    }
+    if (cudaSetDevice(s->m->device) != cudaSuccess) return RLT_E_DEVICE;
+    if (!is_device_ptr(scores) || !is_device_ptr(parents) || !is_device_ptr(tokens) ||
+        (finished && !is_device_ptr(finished)))
+        return RLT_E_ARG;
+    if (!s->beam_scores)
+        if (int rc = salloc(s, (void**)&s->beam_scores, (size_t)s->B * 4)) return rc;
+    if (!s->beam_fin)
+        if (int rc = salloc(s, (void**)&s->beam_fin, (size_t)s->B)) return rc;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const size_t B = s->B;
+    readout_logits(s, s->logits, st);
+    int rc = launch_status();
+    if (rc) return rc;
+    if (rlt::launch_beam_select<float>(s->logits, scores, finished, eos, temperature,
+                                       s->B / beams, beams, c.vocab, beams, parents, tokens,
+                                       s->beam_scores, finished ? s->beam_fin : nullptr,
+                                       st) != cudaSuccess) {
+        cudaGetLastError();
+        return RLT_E_DEVICE;
+    }
+    if (cudaMemcpyAsync(scores, s->beam_scores, B * 4, cudaMemcpyDeviceToDevice, st) ||
+        (finished && cudaMemcpyAsync(finished, s->beam_fin, B, cudaMemcpyDeviceToDevice, st)))
+        return RLT_E_DEVICE;
+    rc = reorder_rows(s, parents, beams, shared, st);
+    if (rc == RLT_OK) rc = rlt_encode(s, tokens, 1, stream);
+    if (rc == RLT_OK) rc = run_block(s, 1, st);
+    return rc;
+}
+
+// ============================================================================
 // reset, positions, export, errors
 // ============================================================================
 extern "C" int rlt_state_reset(rlt_state* s, const int32_t* rows, int n, void* stream) {
@@ -1553,6 +1744,13 @@ extern "C" int rlt_state_positions(const rlt_state* s, int32_t* pos_enc, int32_t
     return RLT_OK;
 }
 
+// bytes of the 8-bit memory's pages
+static size_t mem8_bytes(const rlt_state* s) {
+    const rlt_config& c = s->m->cfg;
+    return (size_t)(c.n_dec > 0 ? c.groups : 0) * s->B * s->mem8_pages * 2 * c.heads * kMem8Page *
+           s->m->dh;
+}
+
 extern "C" int rlt_state_read(rlt_state* s, int part, void* dst, size_t nbytes,
                               size_t* nbytes_out, void* stream) {
     if (!s) return RLT_E_ARG;
@@ -1563,7 +1761,12 @@ extern "C" int rlt_state_read(rlt_state* s, int part, void* dst, size_t nbytes,
         case RLT_PART_S: src = s->s; sz = B * d * 4; break;
         case RLT_PART_R: src = s->Rr; sz = B * d * 4; break;
         case RLT_PART_E: src = s->e; sz = B * s->T_cap * d * 4; break;
-        case RLT_PART_MEM: src = s->mem; sz = B * s->mem_row * elt; break;
+        case RLT_PART_MEM: src = s->mem; sz = s->mem8 ? mem8_bytes(s) : B * s->mem_row * elt; break;
+        case RLT_PART_MEM_SCALES:
+            if (!s->mem8) return RLT_E_UNSUPPORTED;
+            src = s->mem8_scales;
+            sz = mem8_bytes(s) / ((size_t)kMem8Page * s->m->dh) * 4;
+            break;
         case RLT_PART_RING: src = s->ring; sz = B * s->ring_row * elt; break;
         case RLT_PART_ENC: src = s->enc; sz = B * s->enc_row * elt; break;
         default: return RLT_E_ARG;
@@ -1731,6 +1934,7 @@ extern "C" int rlt_state_save(rlt_state* s, int row, void* dst, size_t nbytes,
                               size_t* nbytes_out, void* stream) {
     NvtxRange nvtx("rlt_state_save");
     if (!s || row < 0 || row >= s->B) return RLT_E_ARG;
+    if (s->mem8) return RLT_E_UNSUPPORTED;
     const rlt_model* m = s->m;
     const SnapGeom g = snap_geom(m->cfg);
     const int32_t pe = s->h_pos_enc[row], pd = s->h_pos_dec[row];
@@ -1761,6 +1965,7 @@ extern "C" int rlt_state_load(rlt_state* s, int row, const void* src, size_t nby
                               void* stream) {
     NvtxRange nvtx("rlt_state_load");
     if (!s || !src || row < 0 || row >= s->B) return RLT_E_ARG;
+    if (s->mem8) return RLT_E_UNSUPPORTED;
     const rlt_model* m = s->m;
     if (cudaSetDevice(m->device) != cudaSuccess) return RLT_E_DEVICE;
     const cudaStream_t st = (cudaStream_t)stream;
