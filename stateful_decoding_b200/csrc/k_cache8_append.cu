@@ -11,12 +11,13 @@
 // scale grows as tokens arrive is brought to the new one exactly (e4m3
 // exponents shift), but for values that fall into the subnormal range.
 //
-// A thread holds 8 values of one token: dims a..a+3 and b..b+3 where, in the
-// half layout, b = a + rot/2 (the rotation partners), else b = a + 4.  An item
-// of m tokens has m * dh/8 such units, spread over T threads, NIT units each:
-// one warp per item (four items per CTA) up to 128 units -- generated tokens
-// and short blocks, where 256-thread items left most threads idle -- and 256
-// threads beyond.
+// A thread holds units of 2V values of one token: dims a..a+V-1 and b..b+V-1
+// where, in the half layout, b = a + rot/2 (the rotation partners), else
+// b = a + V.  V = 8 (16-byte loads of bf16), or 4 where rot is no multiple
+// of 16.  An item of m tokens has m * dh/2V such units, spread
+// over T threads, NIT units each: one warp per item (four items per CTA) up to
+// 128 units -- generated tokens and short blocks, where 256-thread items left
+// most threads idle -- and 256 threads beyond.
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -29,22 +30,32 @@ namespace {
 
 constexpr int kLeastExp = -110, kMostExp = 120;
 
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// V (8 or 4) values on 16 (8, for 4 of bf16) bytes
+template <int V>
+__device__ __forceinline__ void load(const float* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
 }
-__device__ __forceinline__ void load4(const bf16* p, float (&x)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
+__device__ __forceinline__ void unpack2(uint32_t w, float* x) {
+    x[0] = __uint_as_float(w << 16);
+    x[1] = __uint_as_float(w & 0xffff0000u);
 }
-
-// largest magnitude with infinities as the largest finite value and NaN as 0
-__device__ __forceinline__ float mag(float x) { return fminf(fabsf(x), FLT_MAX); }
-__device__ __forceinline__ float max_mag(float m, float x) {
-    return x == x ? fmaxf(m, mag(x)) : m;
+template <int V>
+__device__ __forceinline__ void load(const bf16* p, float* x) {
+    if constexpr (V == 8) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        unpack2(v.x, x);
+        unpack2(v.y, x + 2);
+        unpack2(v.z, x + 4);
+        unpack2(v.w, x + 6);
+    } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        unpack2(v.x, x);
+        unpack2(v.y, x + 2);
+    }
 }
 
 // smallest 2^e with amax <= 448 * 2^e = 1.75 * 2^(e+8), e in [least, most]
@@ -72,21 +83,32 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
     return to_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-// where the two groups of four of unit u (of dh/8) sit, and whether they turn
+template <int V>
+__device__ __forceinline__ void to_bytes(uint8_t* p, const float* x, float f) {
+    const uint32_t lo = to_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(lo, to_e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
+    else
+        *reinterpret_cast<uint32_t*>(p) = lo;
+}
+
+// where the two halves of unit u of a token sit, and its first angle (-1: unrotated)
 struct Unit {
-    int a, b, ang;      // ang: first angle index, -1 unrotated
+    int a, b, ang;
 };
+template <int V>
 __device__ __forceinline__ Unit unit_of(int u, int rot, bool inter) {
-    if (inter || 8 * u >= rot) return {8 * u, 8 * u + 4, 8 * u < rot ? 4 * u : -1};
-    return {4 * u, 4 * u + rot / 2, 4 * u};
+    if (inter || 2 * V * u >= rot) return {2 * V * u, 2 * V * u + V, 2 * V * u < rot ? V * u : -1};
+    return {V * u, V * u + rot / 2, V * u};
 }
 
 // T threads per item, NIT units a thread; kItems items per CTA
-template <typename T_, int T, int NIT>
+template <typename T_, int V, int T, int NIT>
 __global__ void __launch_bounds__(T == 32 ? 128 : T)
 k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __restrict__ start,
-                const int32_t* __restrict__ counts, int n, int row_blocks, int n_items,
-                Rope8 rope) {
+                const int32_t* __restrict__ counts, int n, int page_log2, int row_blocks,
+                int n_items, Rope8 rope) {
     constexpr int kItems = T == 32 ? 4 : 1;
     pdl_enter();
     const int sub = T == 32 ? (int)threadIdx.x >> 5 : 0, tid = (int)threadIdx.x - sub * T;
@@ -100,16 +122,16 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
     auto say = [&](int code) {
         if (first && c.status) atomicCAS(c.status, 0, code);
     };
-    const int cap = c.row_pages * c.page;
+    const int page = 1 << page_log2, cap = c.row_pages << page_log2;
     if (cnt < 0 || cnt > n || s0 < 0 || s0 > cap || cnt > cap - s0) {
         // the tokens within the capacity are still written when the counts are sane
         if (j == 0) say(c.cap_code);
         if (cnt < 0 || cnt > n || s0 < 0 || s0 >= cap) return;
     }
     const int end = min(cap, s0 + cnt);
-    const int block = s0 / c.page + j;
-    int lo = max(s0, block * c.page);
-    int hi = min(end, (block + 1) * c.page);
+    const int block = (s0 >> page_log2) + j;
+    int lo = max(s0, block << page_log2);
+    int hi = min(end, (block + 1) << page_log2);
     const Rope8 r = rope;
     if (r.rot) {                                     // positions without a row in the table
         const int plo = -r.origin, phi = r.positions - r.origin;
@@ -118,47 +140,45 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
         hi = min(hi, phi);
     }
     if (lo >= hi) return;
+    // (used only after the loads below: its latency overlaps theirs)
     const int pg = __ldg(c.table + (size_t)row * c.row_pages + block);
-    if (pg < 0 || pg >= c.n_pages) {
-        say(c.arg_code);
-        return;
-    }
-    const int dh = c.dh, upt = dh >> 3;              // units per token
-    const int units = (hi - lo) * upt;
+    const int dh = c.dh, upt_log2 = (dh == 128 ? 7 : 6) - (V == 8 ? 4 : 3);
+    const int upt = 1 << upt_log2;                   // units per token
+    const int units = (hi - lo) << upt_log2;
     const Tok8<const T_> src = kv ? v : k;
     const T_* base = src.p + (int64_t)row * src.row + (int64_t)(lo - s0) * src.token +
                      (int64_t)h * dh;
     const int rot = kv ? 0 : r.rot;
     const bool inter = r.interleaved != 0;
 
-    float x[NIT][8];
+    float x[NIT][2 * V];
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
         const int w = tid + i * T;
         if (w < units) {
-            const Unit un = unit_of(w % upt, rot, inter);
-            const T_* p = base + (int64_t)(w / upt) * src.token;
-            load4(p + un.a, *reinterpret_cast<float(*)[4]>(&x[i][0]));
-            load4(p + un.b, *reinterpret_cast<float(*)[4]>(&x[i][4]));
+            const Unit un = unit_of<V>(w & (upt - 1), rot, inter);
+            const T_* p = base + (int64_t)(w >> upt_log2) * src.token;
+            load<V>(p + un.a, x[i]);
+            load<V>(p + un.b, x[i] + V);
         }
     }
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
         const int w = tid + i * T;
         if (w < units) {
-            const Unit un = unit_of(w % upt, rot, inter);
+            const Unit un = unit_of<V>(w & (upt - 1), rot, inter);
             if (un.ang >= 0) {
                 const size_t at =
-                    (size_t)(lo + w / upt + r.origin) * (rot >> 1) + (size_t)un.ang;
-                float cs[4], sn[4];
-                load4(r.cs + at, cs);
-                load4(r.sn + at, sn);
+                    (size_t)(lo + (w >> upt_log2) + r.origin) * (rot >> 1) + (size_t)un.ang;
+                float cs[V], sn[V];
+                load<V>(r.cs + at, cs);
+                load<V>(r.sn + at, sn);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // pair q: (x[q], x[q+4]) in the half layout, (x[2q], x[2q+1]) interleaved
+                for (int q = 0; q < V; ++q) {
+                    // pair q: (x[q], x[q+V]) in the half layout, (x[2q], x[2q+1]) interleaved
                     const float x1 = inter ? x[i][2 * q] : x[i][q];
-                    const float x2 = inter ? x[i][2 * q + 1] : x[i][q + 4];
+                    const float x2 = inter ? x[i][2 * q + 1] : x[i][q + V];
                     // rounded one by one, not contracted: the bytes do not depend on
                     // how a compiler fuses the pair
                     const float y1 = __fsub_rn(__fmul_rn(x1, cs[q]), __fmul_rn(x2, sn[q]));
@@ -168,13 +188,17 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
                         x[i][2 * q + 1] = y2;
                     } else {
                         x[i][q] = y1;
-                        x[i][q + 4] = y2;
+                        x[i][q + V] = y2;
                     }
                 }
             }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) amax = max_mag(amax, x[i][q]);
+            for (int q = 0; q < 2 * V; ++q) amax = fmaxf(amax, fabsf(x[i][q]));   // skips NaN
         }
+    }
+    if (pg < 0 || pg >= c.n_pages) {                 // the same for the whole item
+        say(c.arg_code);
+        return;
     }
     amax = warp_max(amax);
     if constexpr (T > 32) {
@@ -184,9 +208,10 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
 #pragma unroll
         for (int i = 0; i < T / 32; ++i) amax = fmaxf(amax, s_max[i]);
     }
+    amax = fminf(amax, FLT_MAX);                     // infinities as the largest finite value
     float* scale_at = c.scales + ((size_t)pg * 2 + kv) * c.kv_heads + h;
-    uint8_t* page = c.pages + (((size_t)pg * 2 + kv) * c.kv_heads + h) * (size_t)c.page * dh;
-    const int slot0 = lo - block * c.page, kept = s0 - block * c.page;
+    uint8_t* bytes = c.pages + (((size_t)pg * 2 + kv) * c.kv_heads + h) * (size_t)(page * dh);
+    const int slot0 = lo - block * page, kept = s0 - block * page;
     float scale = pow2_scale(amax);
     if (kept > 0) {                                  // the row's earlier tokens in this page
         const float old = __ldcg(scale_at);
@@ -196,7 +221,7 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
             scale = old;
         } else if (old > 0.f) {
             const float f = old / scale;
-            uint4* q = reinterpret_cast<uint4*>(page);
+            uint4* q = reinterpret_cast<uint4*>(bytes);
             for (int i = tid; i < kept * dh / 16; i += T) {
                 uint4 w = q[i];
                 w.x = rescale4(w.x, f);
@@ -209,17 +234,15 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
     }
     if (tid == 0) *scale_at = scale;
     const float inv = 1.f / scale;                   // exact for powers of two
-    uint8_t* dst = page + (size_t)slot0 * dh;
+    uint8_t* dst = bytes + (size_t)slot0 * dh;
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
         const int w = tid + i * T;
         if (w < units) {
-            const Unit un = unit_of(w % upt, rot, inter);
-            uint8_t* p = dst + (size_t)(w / upt) * dh;
-            *reinterpret_cast<uint32_t*>(p + un.a) =
-                to_e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-            *reinterpret_cast<uint32_t*>(p + un.b) =
-                to_e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+            const Unit un = unit_of<V>(w & (upt - 1), rot, inter);
+            uint8_t* p = dst + (w >> upt_log2) * dh;
+            to_bytes<V>(p + un.a, x[i], inv);
+            to_bytes<V>(p + un.b, x[i] + V, inv);
         }
     }
 }
@@ -235,20 +258,25 @@ cudaError_t launch_cache8_append(const Cache8& c, Tok8<const T> k, Tok8<const T>
     const int row_blocks = (int)std::min<int64_t>(c.row_pages, ((int64_t)n + c.page - 2) / c.page + 1);
     const int64_t items = (int64_t)c.rows * row_blocks * c.kv_heads * 2;
     if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const int units = std::min(n, c.page) * (c.dh / 8);
+    int page_log2 = 4;
+    while ((1 << page_log2) < c.page) ++page_log2;
     auto go = [&](auto kern, int threads, int per_cta) {
-        cudaError_t e = launch(kern, (unsigned)((items + per_cta - 1) / per_cta), threads, 0, st, c, k, v, start,
-                               counts, n, row_blocks, (int)items, rope);
+        cudaError_t e = launch(kern, (unsigned)((items + per_cta - 1) / per_cta), threads, 0, st, c,
+                               k, v, start, counts, n, page_log2, row_blocks, (int)items, rope);
         if (e == cudaSuccess) rlt_count_launch();
         return e;
     };
-    if (units <= 32) return go(k_cache8_append<T, 32, 1>, 128, 4);
-    if (units <= 64) return go(k_cache8_append<T, 32, 2>, 128, 4);
-    if (units <= 128) return go(k_cache8_append<T, 32, 4>, 128, 4);
-    if (units <= 256) return go(k_cache8_append<T, 256, 1>, 256, 1);
-    if (units <= 512) return go(k_cache8_append<T, 256, 2>, 256, 1);
-    if (units <= 1024) return go(k_cache8_append<T, 256, 4>, 256, 1);
-    return go(k_cache8_append<T, 256, 8>, 256, 1);
+    const bool wide = rope.rot % 16 == 0;            // else a unit of 16 would turn in part
+    const int units = std::min(n, c.page) * (c.dh / (wide ? 16 : 8));
+    if (wide) {
+        if (units <= 64) return go(k_cache8_append<T, 8, 32, 2>, 128, 4);
+        if (units <= 128) return go(k_cache8_append<T, 8, 32, 4>, 128, 4);
+        if (units <= 512) return go(k_cache8_append<T, 8, 256, 2>, 256, 1);
+        return go(k_cache8_append<T, 8, 256, 4>, 256, 1);
+    }
+    if (units <= 128) return go(k_cache8_append<T, 4, 32, 4>, 128, 4);
+    if (units <= 1024) return go(k_cache8_append<T, 4, 256, 4>, 256, 1);
+    return go(k_cache8_append<T, 4, 256, 8>, 256, 1);
 }
 
 template cudaError_t launch_cache8_append<float>(const Cache8&, Tok8<const float>,
