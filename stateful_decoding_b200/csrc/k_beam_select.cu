@@ -4,27 +4,31 @@
 //
 // Within a beam the order of c is the order of x, so a beam's own k best
 // logits (and its log-sum) are all that the group has to compare.  The work is
-// one read of the logits, bound by HBM: a unit is one beam, or a slice of one
-// where a group has fewer than 8 beams, and a cluster of up to 8 CTAs holds a
-// group's units.
+// one read of the logits, bound by HBM for batches of searches: a unit is one
+// beam, or a slice of one where a group has fewer than 8 beams, and a cluster
+// of up to 8 CTAs (16 for a few searches) holds a group's units.
 //
-//   scan    each thread reads 16-byte chunks tid, tid + 512, ... of its unit
-//           and keeps the largest logit it saw, and sum 2^((x - m) log2(e)/T)
-//           against its own running maximum m (rescaled when m rises).
-//   cut     the k-th largest of the threads' maxima bounds the k-th best logit
-//           from below: the k best of the unit lie among the few threads whose
-//           maximum reaches it.  Those threads' chunks alone are read again
-//           (from L2) and their logits >= the cut collected: about k of them,
-//           ranked by counting.  When ties leave more than the buffer holds,
-//           the k best are drawn one by one by scanning the unit k times.
-//   join    the units' sorted lists meet in the cluster's first CTA; one warp
-//           merges them with c in fp64.
+//   scan    each thread reads 16-byte chunks tid, tid + 512, ... of its unit,
+//           eight in flight, and keeps the largest logit it saw, and
+//           sum 2^((x - m) log2(e)/T) against its own running maximum m
+//           (rescaled when m rises, four chunks at a time).
+//   cut     the k-th largest of the maxima of 128 groups of four threads
+//           bounds the k-th best logit from below: the k best of the unit lie
+//           among the few threads whose maximum reaches it.  Those threads'
+//           chunks alone are read again (from L2) and their logits >= the cut
+//           collected: about k of them, ranked by counting.  When ties leave
+//           more than the buffer holds, the k best are drawn one by one by
+//           scanning the unit k times.
+//   join    the units write their sorted lists into the first CTA's shared
+//           memory and leave; it forms c in fp64 and ranks the candidates, by
+//           counting up to 512 of them, else by one warp's merge.
 //
 // The exponent (x - m) log2(e)/T takes log2(e)/T in two parts and threads' sums
 // are added in fp64: the error of the log-sum is that of single exponentials
 // averaged over the vocabulary (about 1e-8), so beams compare as in exact
 // arithmetic down to that distance.
 #include <cooperative_groups.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -37,9 +41,10 @@ namespace rlt {
 namespace {
 
 constexpr int NT = 512, NW = NT / 32;
+constexpr int NB = 4;                   // chunks per step of a thread
 constexpr int kCand = 1024;             // candidates a unit may collect
-constexpr int kMaxUnits = 8;            // units of one CTA: beams <= 64 over 8 CTAs
 constexpr int kSliceMin = 4096;         // logits of a slice at least
+constexpr int kMostUnits = kMaxBeams;   // of a group
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -47,30 +52,82 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// order-preserving key of a float (no NaN)
+// order-preserving key of a float (no NaN), and back
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t u = __float_as_uint(x);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+__device__ __forceinline__ float float_of(uint32_t key) {
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
 
+// two fp32 values in one register pair: one instruction for both
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// 16 bytes of logits; clean: NaN becomes -inf; top: the largest; get: elements 2i, 2i + 1
 template <typename T> struct Chunk;
 template <> struct Chunk<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    static constexpr uint32_t kNone = 0xff800000u;      // -inf in every element
+    static __device__ __forceinline__ void clean(uint4& v) {
+        uint32_t* w = &v.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(fmaxf(__uint_as_float(w[i]), -INFINITY));
+    }
+    static __device__ __forceinline__ float top(const uint4& v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    static __device__ __forceinline__ float2 get(const uint4& v, int i) {
+        return i ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w))
+                 : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
     }
 };
 template <> struct Chunk<bf16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const bf16* p, float (&x)[8]) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    static constexpr uint32_t kNone = 0xff80ff80u;
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ void clean(uint4& v) {
+        v.x = max2(v.x, kNone);
+        v.y = max2(v.y, kNone);
+        v.z = max2(v.z, kNone);
+        v.w = max2(v.w, kNone);
+    }
+    static __device__ __forceinline__ float top(const uint4& v) {
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    static __device__ __forceinline__ float2 get(const uint4& v, int i) {
+        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
 };
 
@@ -81,26 +138,40 @@ struct Span {
     static constexpr int N = Chunk<T>::N;
     const T* row;           // element 0 of the row
     int lo, hi, first;      // first: element index of chunk 0's start (<= lo)
-    int chunks;
+    int chunks, whole0, whole1;     // chunks [whole0, whole1) are whole
     __device__ Span(const T* r, int lo_, int hi_) : row(r), lo(lo_), hi(hi_) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(r + lo);
         first = lo - (int)((a & 15) / sizeof(T));
         chunks = hi > lo ? (hi - first + N - 1) / N : 0;
+        whole0 = first < lo ? 1 : 0;
+        whole1 = chunks - (first + chunks * N > hi ? 1 : 0);
     }
-    // chunk ci; elements outside [lo, hi) and NaN come out as -inf
+    // chunk ci where whole, else nothing but -inf
+    __device__ __forceinline__ uint4 fetch(int ci) const {
+        constexpr uint32_t z = Chunk<T>::kNone;
+        uint4 v = make_uint4(z, z, z, z);
+        if (ci >= whole0 && ci < whole1)
+            v = __ldg(reinterpret_cast<const uint4*>(row + first + (int64_t)ci * N));
+        return v;
+    }
+    // any chunk; elements outside [lo, hi) and NaN come out as -inf
     __device__ __forceinline__ void load(int ci, float (&x)[N]) const {
-        const int e0 = first + ci * N;
-        if (e0 >= lo && e0 + N <= hi) {
-            Chunk<T>::load(row + e0, x);
+        if (ci >= whole0 && ci < whole1) {
+            uint4 v = fetch(ci);
+            Chunk<T>::clean(v);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float2 f = Chunk<T>::get(v, i);
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            }
         } else {
+            const int e0 = first + ci * N;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 x[i] = -INFINITY;
-                if (e0 + i >= lo && e0 + i < hi) x[i] = to_f(row[e0 + i]);
+                if (e0 + i >= lo && e0 + i < hi) x[i] = fmaxf(to_f(row[e0 + i]), -INFINITY);
             }
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = fmaxf(x[i], -INFINITY);   // NaN: -inf
     }
 };
 
@@ -125,42 +196,44 @@ k_beam_select(const T* __restrict__ logits, const float* __restrict__ scores,
               int vocab, int slices, int k, int32_t* __restrict__ parents,
               int32_t* __restrict__ tokens, float* __restrict__ new_scores,
               uint8_t* __restrict__ new_finished) {
-    constexpr int N = Chunk<T>::N;
-    extern __shared__ __align__(16) uint8_t dyn[];      // candidates, then the join's lists
-    __shared__ Entry s_list[kMaxUnits][kMaxBeams];
-    __shared__ Unit s_unit[kMaxUnits];
-    __shared__ float s_best[NT];
-    __shared__ int s_pick[NT];
+    constexpr int N = Chunk<T>::N, GROUPS = NT / 4;
+    extern __shared__ __align__(16) uint8_t dyn[];      // candidates; in rank 0 the units' lists
+    __shared__ Unit s_unit[kMostUnits];                 // rank 0: every unit's
+    __shared__ uint32_t s_key[GROUPS];
+    __shared__ float s_best[NW];
     __shared__ double s_sum[NW];
     __shared__ float s_m[NW];
     __shared__ int s_at[NW];
-    __shared__ int s_n, s_picks;
+    __shared__ int s_n;
+    __shared__ uint32_t s_cut;
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int group = (int)(blockIdx.x / (unsigned)C);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int units = beams * slices;
-    if (rank >= units) return;                          // never rank 0
+    const int units = beams * slices;                   // C <= units
     Entry* cand = reinterpret_cast<Entry*>(dyn);
+    Entry* all = cand + kCand;                          // rank 0: [units][k]
+    Unit* to_unit = cluster.map_shared_rank(s_unit, 0);
+    Entry* to_list = cluster.map_shared_rank(all, 0);
 
     const double c64 = 1.4426950408889634 / (double)temperature;
-    const float c_hi = (float)c64, c_lo = (float)(c64 - (double)c_hi);
-    auto e2 = [&](float d) {                            // (the bound keeps 0 x inf out)
-        d = fmaxf(d, -1e16f);
-        return ex2(fmaf(d, c_hi, d * c_lo));
-    };
+    // both parts positive, so that -inf x either stays -inf
+    const float c_hi = __double2float_rd(c64), c_lo = fmaxf((float)(c64 - (double)c_hi), FLT_MIN);
+    auto e2 = [&](float d) { return ex2(fmaf(d, c_hi, d * c_lo)); };
+    const uint64_t hi2 = pair(c_hi, c_hi), lo2 = pair(c_lo, c_lo);
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");    // every CTA runs: rank 0 takes writes
 
-    int mine = 0;
-    for (int u = rank; u < units; u += C, ++mine) {
+    for (int u = rank; u < units; u += C) {
         const int b = u / slices, sl = u % slices;
         const float score = __ldg(scores + (size_t)group * beams + b);
         const bool fin = finished && __ldg(finished + (size_t)group * beams + b);
         const bool sane = fabsf(score) < INFINITY;
         if (fin || !sane) {                             // nothing to read
             if (tid == 0) {
-                s_unit[mine] = {0.f, fin && sl == 0 && sane ? 1 : 0, 1.0};
-                s_list[mine][0] = {0.f, eos};
+                to_unit[u] = {0.f, fin && sl == 0 && sane ? 1 : 0, 1.0};
+                to_list[u * k] = {0.f, eos};
             }
             continue;
         }
@@ -168,72 +241,109 @@ k_beam_select(const T* __restrict__ logits, const float* __restrict__ scores,
         const Span<T> span(logits + ((size_t)group * beams + b) * vocab, min(vocab, sl * len),
                            min(vocab, (sl + 1) * len));
         // ------------------------------------------------------------ scan
-        float m = -INFINITY, s = 0.f;
-        auto take = [&](const float (&x)[N]) {
-            float cm = x[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) cm = fmaxf(cm, x[i]);
-            if (cm > m) {
-                s *= e2(m - cm);                        // m = -inf: 0 x 0
-                m = cm;
-            }
-            if (m > -INFINITY) {
-                float t = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; ++i) t += e2(x[i] - m);
-                s += t;
+        float m = -INFINITY;
+        uint64_t s2 = pair(0.f, 0.f);
+        auto rise = [&](float top) {
+            if (top > m) {
+                const float f = m > -INFINITY ? e2(m - top) : 0.f;
+                s2 = mul2(s2, pair(f, f));
+                m = top;
             }
         };
-        int ci = tid;
-        for (; ci + 3 * NT < span.chunks; ci += 4 * NT) {   // four loads in flight
-            float x[4][N];
+        const int steps = (span.chunks + NB * NT - 1) / (NB * NT);
+        uint4 next[NB];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) span.load(ci + q * NT, x[q]);
+        for (int q = 0; q < NB; ++q) next[q] = span.fetch(tid + q * NT);
+        for (int i = 0; i < steps; ++i) {
+            uint4 v[NB];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) take(x[q]);
+            for (int q = 0; q < NB; ++q) {
+                v[q] = next[q];
+                next[q] = span.fetch(tid + ((i + 1) * NB + q) * NT);
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < NB; ++q) {
+                Chunk<T>::clean(v[q]);
+                top = fmaxf(top, Chunk<T>::top(v[q]));
+            }
+            rise(top);
+            if (m > -INFINITY) {
+                const uint64_t m2 = pair(-m, -m);
+                uint64_t t2 = pair(0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < NB; ++q)
+#pragma unroll
+                    for (int x = 0; x < N / 2; ++x) {
+                        const float2 f = Chunk<T>::get(v[q], x);
+                        const uint64_t d = add2(pair(f.x, f.y), m2);
+                        const float2 e = unpair(fma2(d, hi2, mul2(d, lo2)));
+                        t2 = add2(t2, pair(ex2(e.x), ex2(e.y)));
+                    }
+                s2 = add2(s2, t2);
+            }
         }
-        for (; ci < span.chunks; ci += NT) {
-            float x[N];
-            span.load(ci, x);
-            take(x);
+        const float2 halves = unpair(s2);
+        float s = halves.x + halves.y;
+        for (int end = 0; end < 2; ++end) {             // the partial chunks at the ends
+            const int ci = end ? span.whole1 : 0;
+            const bool part = end ? ci < span.chunks && !(ci == 0 && span.whole0) : span.whole0 == 1;
+            if (part && span.chunks > 0 && ci % NT == tid) {
+                float x[N];
+                span.load(ci, x);
+                for (int q = 0; q < N; ++q) {
+                    if (x[q] > m) {
+                        s = m > -INFINITY ? s * e2(m - x[q]) : 0.f;
+                        m = x[q];
+                    }
+                    if (m > -INFINITY) s += e2(x[q] - m);
+                }
+            }
         }
-        // ------------------------------------------------------------ the unit's maximum and sum
-        const float wm = warp_max(m);
-        if (lane == 0) s_m[warp] = wm;
-        if (tid == 0) s_n = 0, s_picks = 0;
-        __syncthreads();
-        float M = s_m[0];
-#pragma unroll
-        for (int i = 1; i < NW; ++i) M = fmaxf(M, s_m[i]);
-        double ds = m > -INFINITY ? (double)(s * e2(m - M)) : 0.0;
+        // ------------------------------------------------------------ the warps' maxima and sums
+        const uint32_t key = key_of(m);
+        const float wm = float_of(__reduce_max_sync(0xffffffffu, key));
+        double ds = m > -INFINITY ? (double)(s * e2(m - wm)) : 0.0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
-        if (lane == 0) s_sum[warp] = ds;
-        const bool dead = !(M > -INFINITY) || M == INFINITY;
-        // ------------------------------------------------------------ cut
-        // the k-th largest of the threads' maxima, found bit by bit on their keys
-        const uint32_t key = key_of(m);
-        uint32_t cut = 0;
-        if (!dead)
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t at = cut | (1u << bit);
-                if (__syncthreads_count(key >= at) >= k) cut = at;
-            }
-        __syncthreads();                                // s_sum is there too
-        if (tid == 0) {
-            double sum = 0.0;
-            for (int i = 0; i < NW; ++i) sum += s_sum[i];
-            s_unit[mine] = {M, 0, sum};
-        }
-        if (dead) {
-            __syncthreads();
-            continue;
-        }
-        if (key >= cut && m > -INFINITY) s_pick[atomicAdd(&s_picks, 1)] = tid;
+        if (lane == 0) s_m[warp] = wm, s_sum[warp] = ds;
+        uint32_t gk = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        gk = max(gk, __shfl_xor_sync(0xffffffffu, gk, 2));
+        if ((lane & 3) == 0) s_key[tid >> 2] = gk;
+        if (tid == 0) s_n = 0;
         __syncthreads();
-        const int picks = s_picks;
-        for (int p = warp; p < picks; p += NW) {
-            const int who = s_pick[p];
+        // ------------------------------------------------------------ cut
+        if (warp == 0) {                                // the k-th largest of the groups' maxima
+            uint32_t mine[GROUPS / 32], cut = 0;
+#pragma unroll
+            for (int i = 0; i < GROUPS / 32; ++i) mine[i] = s_key[lane + 32 * i];
+            for (int i = 0; i < k; ++i) {
+                uint32_t best = mine[0];
+#pragma unroll
+                for (int j = 1; j < GROUPS / 32; ++j) best = max(best, mine[j]);
+                cut = __reduce_max_sync(0xffffffffu, best);
+                const uint32_t who = __ballot_sync(0xffffffffu, best == cut);
+                if (lane == __ffs(who) - 1) {           // one of them is taken
+                    bool gone = false;
+#pragma unroll
+                    for (int j = 0; j < GROUPS / 32; ++j)
+                        if (!gone && mine[j] == cut) mine[j] = 0, gone = true;
+                }
+            }
+            if (lane == 0) s_cut = cut;
+        } else if (warp == 1) {
+            const float pm = lane < NW ? s_m[lane] : -INFINITY;
+            const float M = float_of(__reduce_max_sync(0xffffffffu, key_of(pm)));
+            double sum = lane < NW && pm > -INFINITY ? s_sum[lane] * (double)e2(pm - M) : 0.0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) to_unit[u].m = M, to_unit[u].sum = sum;
+        }
+        __syncthreads();
+        const uint32_t cut = s_cut;
+        for (uint32_t left = __ballot_sync(0xffffffffu, key >= cut && m > -INFINITY); left;
+             left &= left - 1) {
+            const int who = warp * 32 + __ffs(left) - 1;
             for (int c0 = who + lane * NT; c0 < span.chunks; c0 += 32 * NT) {
                 float x[N];
                 span.load(c0, x);
@@ -252,9 +362,9 @@ k_beam_select(const T* __restrict__ logits, const float* __restrict__ scores,
                 const Entry me = cand[i];
                 int place = 0;
                 for (int j = 0; j < n; ++j) place += before(cand[j].x, cand[j].v, me.x, me.v);
-                if (place < k) s_list[mine][place] = me;
+                if (place < k) to_list[u * k + place] = me;
             }
-            if (tid == 0) s_unit[mine].count = min(n, k);
+            if (tid == 0) to_unit[u].count = min(n, k);
         } else {
             // more ties at the cut than the buffer holds: one by one
             float px = INFINITY;
@@ -283,96 +393,114 @@ k_beam_select(const T* __restrict__ logits, const float* __restrict__ scores,
                 bx = s_best[0], bv = s_at[0];
                 for (int w = 1; w < NW; ++w)
                     if (before(s_best[w], s_at[w], bx, bv)) bx = s_best[w], bv = s_at[w];
-                if (tid == 0) s_list[mine][i] = {bx, bv};
+                if (tid == 0) to_list[u * k + i] = {bx, bv};
                 px = bx, pv = bv;
             }
-            if (tid == 0) s_unit[mine].count = k;       // n > kCand >= k: all are finite
+            if (tid == 0) to_unit[u].count = k;         // n > kCand >= k: all are finite
         }
-        __syncthreads();
+        __syncthreads();                                // cand, s_key, s_n serve the next unit
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank) return;                                   // their lists are in rank 0
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // ------------------------------------------------------------ join
+    __shared__ double s_base[kMaxBeams], s_top[kMaxBeams];
+    __shared__ bool s_open[kMaxBeams], s_fin[kMaxBeams];
+    if (tid < beams) {                                  // c = base + (x - top) / T
+        const int b = tid;
+        double base = (double)__ldg(scores + (size_t)group * beams + b), top = 0.0;
+        const bool fin = finished && __ldg(finished + (size_t)group * beams + b);
+        bool open = true;
+        if (!fin) {
+            float M = -INFINITY;
+            for (int i = 0; i < slices; ++i) M = fmaxf(M, s_unit[b * slices + i].m);
+            double sum = 0.0;
+            for (int i = 0; i < slices; ++i) {
+                const Unit& w = s_unit[b * slices + i];
+                if (w.m > -INFINITY)
+                    sum += w.m == M ? w.sum
+                                    : w.sum * exp(((double)w.m - (double)M) / (double)temperature);
+            }
+            top = (double)M;
+            base -= log(sum);
+            open = fabsf(M) < INFINITY;                 // +inf logits, or none above -inf: closed
+        }
+        s_base[b] = base, s_top[b] = top, s_open[b] = open, s_fin[b] = fin;
     }
     __syncthreads();
-    if (min(C, units) > 1) cluster.sync();              // (ranks without a unit have exited)
-    if (rank == 0) {
-        // ------------------------------------------------------------ join
-        Entry* all = reinterpret_cast<Entry*>(dyn);     // [units][k]
-        __shared__ Unit s_all[kMaxBeams];
-        for (int u = tid; u < units; u += NT) s_all[u] = *cluster.map_shared_rank(&s_unit[u / C], u % C);
-        __syncthreads();
-        for (int i = tid; i < units * k; i += NT) {
-            const int u = i / k, j = i % k;
-            if (j < s_all[u].count) all[i] = *cluster.map_shared_rank(&s_list[u / C][j], u % C);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l merges lists l and l + 32
-            double base[2] = {0.0, 0.0}, head[2];       // c = base + (x - M) / T
-            double top[2] = {0.0, 0.0};
-            int at[2] = {0, 0}, flat[2];
-            bool fin[2] = {false, false};
-            auto load = [&](int q) {
-                const int u = lane + 32 * q;
-                head[q] = -INFINITY;
-                flat[q] = 0x7fffffff;
-                if (u < units && at[q] < s_all[u].count) {
-                    const Entry e = all[u * k + at[q]];
-                    head[q] = base[q] + (fin[q] ? 0.0 : ((double)e.x - top[q]) / (double)temperature);
-                    flat[q] = (u / slices) * vocab + e.v;
-                }
-            };
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int u = lane + 32 * q;
-                if (u < units) {
-                    const int b = u / slices;
-                    base[q] = (double)__ldg(scores + (size_t)group * beams + b);
-                    fin[q] = finished && __ldg(finished + (size_t)group * beams + b);
-                    if (!fin[q]) {
-                        float M = -INFINITY;
-                        for (int i = 0; i < slices; ++i) M = fmaxf(M, s_all[b * slices + i].m);
-                        double sum = 0.0;
-                        for (int i = 0; i < slices; ++i) {
-                            const Unit& w = s_all[b * slices + i];
-                            if (w.m > -INFINITY)
-                                sum += w.sum * exp(((double)w.m - (double)M) / (double)temperature);
-                        }
-                        top[q] = (double)M;
-                        base[q] -= log(sum);
-                        // +inf logits, or none above -inf: no candidate of this beam
-                        if (!(fabsf(M) < INFINITY)) at[q] = k;
-                    }
-                }
-                load(q);
+    auto score_of = [&](int u, const Entry& e) {
+        const int b = u / slices;
+        return s_base[b] + (s_fin[b] ? 0.0 : ((double)e.x - s_top[b]) / (double)temperature);
+    };
+    auto put = [&](int place, double c, int flat, bool none) {
+        const size_t to = (size_t)group * k + place;
+        const int b = none ? 0 : flat / vocab, v = none ? 0 : flat % vocab;
+        parents[to] = b;
+        tokens[to] = v;
+        new_scores[to] = none ? -INFINITY : (float)c;
+        if (new_finished) new_finished[to] = !none && (s_fin[b] || v == eos);
+    };
+    const int total = units * k;
+    if (total <= NT) {
+        __shared__ double s_c[NT];
+        __shared__ int s_flat[NT];
+        double c = -INFINITY;
+        int flat = 0x7fffffff;
+        if (tid < total) {
+            const int u = tid / k;
+            if (s_open[u / slices] && tid % k < s_unit[u].count) {
+                const Entry e = all[tid];
+                c = score_of(u, e);
+                flat = (u / slices) * vocab + e.v;
             }
-            for (int i = 0; i < k; ++i) {
-                const int q = head[1] > head[0] || (head[1] == head[0] && flat[1] < flat[0]);
-                double best = head[q];
-                int bf = flat[q];
-                const int own = bf;
+            s_c[tid] = c;
+            s_flat[tid] = flat;
+        }
+        const int valid = __syncthreads_count(c > -INFINITY);
+        if (c > -INFINITY) {
+            int place = 0;
+            for (int j = 0; j < total; ++j)
+                place += s_c[j] > c || (s_c[j] == c && s_flat[j] < flat);
+            if (place < k) put(place, c, flat, false);
+        }
+        if (tid >= valid && tid < k) put(tid, 0.0, 0, true);
+        return;
+    }
+    if (warp == 0) {
+        // lane l merges lists l and l + 32
+        double head[2];
+        int at[2] = {0, 0}, flat[2];
+        auto load = [&](int q) {
+            const int u = lane + 32 * q;
+            head[q] = -INFINITY;
+            flat[q] = 0x7fffffff;
+            if (u < units && s_open[u / slices] && at[q] < s_unit[u].count) {
+                const Entry e = all[u * k + at[q]];
+                head[q] = score_of(u, e);
+                flat[q] = (u / slices) * vocab + e.v;
+            }
+        };
+        load(0);
+        load(1);
+        for (int i = 0; i < k; ++i) {
+            const int q = head[1] > head[0] || (head[1] == head[0] && flat[1] < flat[0]);
+            double best = head[q];
+            int bf = flat[q];
+            const int own = bf;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-                    const int of = __shfl_xor_sync(0xffffffffu, bf, o);
-                    if (ob > best || (ob == best && of < bf)) best = ob, bf = of;
-                }
-                const bool none = !(best > -INFINITY);
-                if (lane == 0) {
-                    const size_t to = (size_t)group * k + i;
-                    const int b = none ? 0 : bf / vocab, v = none ? 0 : bf % vocab;
-                    parents[to] = b;
-                    tokens[to] = v;
-                    new_scores[to] = none ? -INFINITY : (float)best;
-                    if (new_finished)
-                        new_finished[to] =
-                            !none && ((finished && finished[(size_t)group * beams + b]) || v == eos);
-                }
-                if (!none && own == bf) {               // one lane alone holds that candidate
-                    ++at[q];
-                    load(q);
-                }
+            for (int o = 16; o > 0; o >>= 1) {
+                const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+                const int of = __shfl_xor_sync(0xffffffffu, bf, o);
+                if (ob > best || (ob == best && of < bf)) best = ob, bf = of;
+            }
+            const bool none = !(best > -INFINITY);
+            if (lane == 0) put(i, best, bf, none);
+            if (!none && own == bf) {                   // one lane alone holds that candidate
+                ++at[q];
+                load(q);
             }
         }
     }
-    if (min(C, units) > 1) cluster.sync();              // no CTA leaves while its lists are read
 }
 
 }  // namespace
@@ -387,14 +515,17 @@ cudaError_t launch_beam_select(const T* logits, const float* scores, const uint8
     int slices = 1;
     while (slices * 2 * beams <= 8 && vocab / (slices * 2) >= kSliceMin) slices *= 2;
     const int units = beams * slices;
-    int C = 1;
-    while (C < 8 && C < units) C *= 2;
+    // CTAs of a group: as few as finish in as many turns as 8 would take (fewer idle at the end);
+    // up to 16 where so few searches run that each may spread over more of the machine
+    int most = 8;
+    auto* kern = k_beam_select<T>;
+    const void* kp = reinterpret_cast<const void*>(kern);
+    if (units > 8 && groups <= 8 && set_wide_cluster_once(kp)) most = 16;
+    const int turns = (units + most - 1) / most, C = (units + turns - 1) / turns;
     const int64_t ctas = (int64_t)groups * C;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    auto* kern = k_beam_select<T>;
-    const size_t smem = sizeof(Entry) * (size_t)std::max(kCand, units * k);
-    const void* kp = reinterpret_cast<const void*>(kern);
-    if (!set_smem_once(kp, sizeof(Entry) * kMaxBeams * kMaxBeams))
+    const size_t smem = sizeof(Entry) * (size_t)(kCand + units * k);
+    if (!set_smem_once(kp, sizeof(Entry) * (kCand + kMaxBeams * kMaxBeams)))
         return cudaErrorInvalidConfiguration;
     set_carveout_once(kp);
     cudaLaunchConfig_t cfg = {};
