@@ -44,13 +44,9 @@
 // cluster's distributed shared memory, always in run order: no scratch, no
 // atomics, and the same bits for a row whatever batch or capacity it sits in.
 #include <cooperative_groups.h>
-#include <cuda_fp16.h>
-#include <math.h>
 
 #include <algorithm>
-
-#include "cache8.cuh"
-#include "tc_common.cuh"
+#include "cache8_tile.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -58,122 +54,15 @@ namespace rlt {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 16;               // keys per step of a warp
 constexpr int kKeysPerCta = 1024;
 constexpr int kMaxCtas = 16;            // CTAs per (row, key head, query tile): one cluster
-constexpr float kLag = 8.f;             // how far (log2) a score may pass the maximum
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// four e4m3 bytes as two pairs of fp16 values, exactly (NaN stays NaN)
-__device__ __forceinline__ void h2x2_of(uint32_t four, uint32_t& lo, uint32_t& hi) {
-    asm("{\n"
-        ".reg .b16 a, b;\n"
-        "mov.b32 {a, b}, %2;\n"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n"
-        "}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(four));
-}
-// the transpose of an 8x8 matrix of fp16 held two to a lane
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_h2(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-// the bits below fp16's 11, times 2^11
-__device__ __forceinline__ uint32_t rest_h2(float lo, float hi, uint32_t lead) {
-    const float2 f = unpack_h2(lead);
-    return pack_h2((lo - f.x) * 2048.f, (hi - f.y) * 2048.f);
-}
-
-template <typename TQ>
-struct QIn {
-    const TQ* p;
-    int64_t row, token;
-    int slabs;              // partial sums to add (1: q itself)
-    size_t slab;
-};
-__device__ __forceinline__ void load4(const QIn<float>& q, size_t at, float (&x)[4]) {
-    float4 v = __ldg(reinterpret_cast<const float4*>(q.p + at));
-    for (int s = 1; s < q.slabs; ++s) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(q.p + (size_t)s * q.slab + at));
-        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-    }
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const QIn<bf16>& q, size_t at, float (&x)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(q.p + at));
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
-// dims d..d+3 (d a multiple of 4) of the query at `at`, rotated at position pos
-template <typename TQ>
-__device__ __forceinline__ void load_q4(const QIn<TQ>& q, size_t at, int d, const Rope8& r, int pos,
-                                        float (&x)[4]) {
-    load4(q, at + d, x);
-    if (d >= r.rot) return;
-    const int half = r.rot >> 1;
-    const float* cs = r.cs + (size_t)pos * half;
-    const float* sn = r.sn + (size_t)pos * half;
-    if (r.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float c = __ldg(cs + d / 2 + e), s = __ldg(sn + d / 2 + e);
-            rope_pair(x[2 * e], x[2 * e + 1], c, s, x[2 * e], x[2 * e + 1]);
-        }
-    } else {
-        const bool low = d < half;
-        const int a = low ? d : d - half;
-        float y[4], unused;
-        load4(q, at + (low ? d + half : d - half), y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float c = __ldg(cs + a + e), s = __ldg(sn + a + e);
-            if (low) rope_pair(x[e], y[e], c, s, x[e], unused);
-            else rope_pair(y[e], x[e], c, s, unused, x[e]);
-        }
-    }
-}
 
 template <int D> constexpr int stages() { return D == 64 ? 4 : 3; }
 template <int D> constexpr int stage_bytes() { return 2 * kTile * D + 16; }
 template <int D> constexpr int ring_bytes() { return kWarps * stages<D>() * stage_bytes<D>(); }
 
-enum Mode { FOLD, SPLIT, PLAIN };
-constexpr int queries_of(int mode, int nb) { return mode == FOLD ? 4 : mode == SPLIT ? 8 : 8 * nb; }
+enum Mode { SPLIT, PLAIN };
+constexpr int queries_of(int mode, int nb) { return mode == SPLIT ? 8 : 8 * nb; }
 
 // CTAs that share a prefix of `keys` keys: a power of two, kKeysPerCta keys each at least
 __host__ __device__ __forceinline__ int ctas_of(int64_t keys) {
@@ -182,7 +71,7 @@ __host__ __device__ __forceinline__ int ctas_of(int64_t keys) {
     return c;
 }
 
-// MODE and NB (products of 8 columns): FOLD 1, SPLIT 2, PLAIN 1 or 2
+// MODE and NB (products of 8 columns): SPLIT 2, PLAIN 1 or 2
 template <int D, int MODE, int NB, typename TQ, typename TO>
 __global__ void __launch_bounds__(kWarps * 32)
 k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int q_tiles,
@@ -241,19 +130,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             }
         }
     };
-    // a lane copies chunk ch of rows cr, cr + RS, ...; where they go in a stage
-    constexpr int CPR = D / 16, RS = 32 / CPR, NK = kTile / RS;     // chunks per row, rows per pass
-    const int cr = lane / CPR, ch = lane % CPR;
-    uint32_t k_off[2], v_off;
-    if constexpr (D == 128) {               // rows cr + 4k -> 2 cr + (k & 1) + 8 (k / 2)
-        k_off[0] = (uint32_t)(2 * cr * D + ch * 16);
-        k_off[1] = (uint32_t)((2 * cr + 1) * D + (ch ^ 1) * 16);
-        v_off = (uint32_t)(kTile * D + cr * D + (ch ^ (cr << 1)) * 16);
-    } else {                                // rows cr + 8k -> 2 (cr & 3) + cr / 4 + 8k
-        k_off[0] = (uint32_t)((((cr & 3) << 1) | (cr >> 2)) * D + ch * 16);
-        k_off[1] = k_off[0] + 8 * D;
-        v_off = (uint32_t)(kTile * D + cr * D + (ch ^ (cr & 2)) * 16);
-    }
+    const TileCopy<D> copy(lane);
     auto issue = [&](int i) {               // tile s_begin + i into stage i % NST
         const int s = s_begin + i;
         if (s < s_end) {
@@ -272,17 +149,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                     make_float4(ks, lv, inv, 0.f);
             const uint8_t* kg = c.pages + ((size_t)max(p, 0) * 2 * c.kv_heads + kvh) * head_bytes +
                                 (size_t)(k0 & ((1 << page_log2) - 1)) * D + lane * 16;
-            const uint8_t* vg = kg + v_bytes;
-            const int left = p >= 0 ? vis_max - k0 : 0;
-            const uint32_t at = ring_u + slot * SB;
-            const bool whole = left >= kTile;
-#pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                const uint32_t kd = D == 128 ? k_off[k & 1] + (k >> 1) * 8 * D : k_off[k];
-                const bool ok = whole || cr + k * RS < left;
-                cp16(at + kd, ok ? kg + k * 512 : c.pages, ok);
-                cp16(at + v_off + k * RS * D, ok ? vg + k * 512 : c.pages, ok);
-            }
+            copy(ring_u + slot * SB, kg, kg + v_bytes, p >= 0 ? vis_max - k0 : 0, c.pages);
         }
         cp_commit();
     };
@@ -316,7 +183,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         if (MODE == SPLIT && b == 1) break;
-        const int r = MODE == FOLD ? g & 3 : 8 * b + g;
+        const int r = 8 * b + g;
         const float* sq = &s_q[r][t * (D / 4)];
         float amax = 0.f;
 #pragma unroll
@@ -331,7 +198,6 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         e2 = max(-100, min(100, e2));
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
-        const bool low = MODE == FOLD && g >= 4;
 #pragma unroll
         for (int k = 0; k < KI; ++k) {
             const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
@@ -339,10 +205,6 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             const uint32_t h0 = pack_h2(x0, x1), h1 = pack_h2(x2, x3);
             qf[k][b][0] = h0;
             qf[k][b][1] = h1;
-            if (MODE == FOLD && low) {
-                qf[k][b][0] = rest_h2(x0, x1, h0);
-                qf[k][b][1] = rest_h2(x2, x3, h1);
-            }
             if (MODE == SPLIT) {
                 qf[k][NB - 1][0] = rest_h2(x0, x1, h0);
                 qf[k][NB - 1][1] = rest_h2(x2, x3, h1);
@@ -350,7 +212,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int col = (2 * t + e) & (MODE == FOLD ? 3 : 7);
+            const int col = 2 * t + e;
             rf[b][e] = __shfl_sync(0xffffffffu, up, 4 * col);
             const int rr = r0 + 8 * b + col, i = rr / share, pos = L - n + i + rope.origin;
             vis[b][e] = rr < nq ? max(0, L - n + i + 1) : 0;
@@ -363,7 +225,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     for (int b = 0; b < NS; ++b)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int col = (2 * t + e) & (MODE == FOLD ? 3 : 7);
+            const int col = 2 * t + e;
             lost |= 8 * b + col < live && vis[b][e] < vis_min;
         }
     const int mask_from = __any_sync(0xffffffffu, lost) ? 0 : vis_min;
@@ -391,9 +253,8 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         for (int b = 0; b < NB; ++b) cf[b][0] = cf[b][1] = cf[b][2] = cf[b][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-            const int kc = D == 128 ? (2 * t + h) ^ (g & 1) : t;
-            const uint4 x = *reinterpret_cast<const uint4*>(st + g * D + kc * 16);
-            const uint4 y = *reinterpret_cast<const uint4*>(st + (g + 8) * D + kc * 16);
+            uint4 x, y;
+            load_keys<D>(st, g, t, h, x, y);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -405,30 +266,11 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                     mma_f16(cf[b], a, qf[4 * h + k][b][0], qf[4 * h + k][b][1]);
             }
         }
-        // values 4i + t, dims [g D/8, (g+1) D/8)
         uint32_t vv[4][D / 32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* vp = st + kTile * D + (4 * i + t) * D;
-            if constexpr (D == 128) {
-                const uint4 v4 = *reinterpret_cast<const uint4*>(vp + ((g ^ (2 * t)) << 4));
-                vv[i][0] = v4.x, vv[i][1] = v4.y, vv[i][2] = v4.z, vv[i][3] = v4.w;
-            } else {
-                const uint2 v2 = *reinterpret_cast<const uint2*>(
-                    vp + (((g >> 1) ^ (t & 2)) << 4) + ((g & 1) << 3));
-                vv[i][0] = v2.x, vv[i][1] = v2.y;
-            }
-        }
+        load_values<D>(st, g, t, vv);
         // scores [key rows g, g + 8][queries 2t, 2t + 1], the value scale folded in
         float s[NS][4];
-        if (MODE == FOLD) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, cf[0][i], 2);
-                const float lead = t < 2 ? cf[0][i] : other, rest = t < 2 ? other : cf[0][i];
-                s[0][i] = fmaf(fmaf(rest, 1.f / 2048.f, lead), rf[0][i & 1] * meta.x, meta.y);
-            }
-        } else if (MODE == SPLIT) {
+        if (MODE == SPLIT) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 s[0][i] = fmaf(fmaf(cf[NB - 1][i], 1.f / 2048.f, cf[0][i]), rf[0][i & 1] * meta.x,
@@ -448,23 +290,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (bad || k0 + key_lo + 8 * (i >> 1) >= vis[b][i & 1]) s[b][i] = -INFINITY;
-            // A value seen by some queries only: a NaN in it would reach the others as
-            // 0 x NaN, so it enters the product as 0 and the weights of those that see it
-            // become NaN.
-            if (mask_from < vis_max) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t hit = 0;
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        const uint32_t z = ((vv[i][x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        hit |= z;
-                        vv[i][x] &= ~((z >> 7) * 0xffu);
-                    }
-                    if (hit) poison |= 1u << (4 * i + t);
-                }
-                poison = __reduce_or_sync(0xffffffffu, poison);
-            }
+            if (mask_from < vis_max) poison = clear_nan<D>(vv, t);
         }
         bool raise = false;
         float mx[NS][2];
@@ -510,12 +336,8 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             for (int h = 0; h < 2; ++h) {
                 const float p0 = p[2 * h], p1 = p[2 * h + 1];
                 const uint32_t lead = pack_h2(p0, p1);
-                if (MODE == FOLD) {
-                    pb[0][h] = transpose8(t < 2 ? lead : rest_h2(p0, p1, lead));
-                } else {
-                    pb[b][h] = transpose8(lead);
-                    if (MODE == SPLIT) pb[NB - 1][h] = transpose8(rest_h2(p0, p1, lead));
-                }
+                pb[b][h] = transpose8(lead);
+                if (MODE == SPLIT) pb[NB - 1][h] = transpose8(rest_h2(p0, p1, lead));
             }
         }
 #pragma unroll
@@ -551,22 +373,18 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     float* cM = cO + QT * D;
     float* cL = cM + QT;
     static_assert((kWarps + 1) * (QT * D + 2 * QT) * 4 <= ring_bytes<D>(), "join fits the ring");
-    if (MODE != PLAIN) {                    // leading and trailing parts
+    if (MODE == SPLIT) {                    // leading and trailing parts
 #pragma unroll
         for (int j = 0; j < VJ; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float rest =
-                    MODE == FOLD ? __shfl_xor_sync(0xffffffffu, O[j][0][i], 2) : O[j][NB - 1][i];
-                O[j][0][i] = fmaf(rest, 1.f / 2048.f, O[j][0][i]);
-            }
+            for (int i = 0; i < 4; ++i) O[j][0][i] = fmaf(O[j][NB - 1][i], 1.f / 2048.f, O[j][0][i]);
     }
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * b + 2 * t + e;
-            if (r < live) {                 // FOLD: the lanes of columns 0-3
+            if (r < live) {
                 float* o = wO + (warp * QT + r) * D + g * (D / 8);
 #pragma unroll
                 for (int j = 0; j < VJ; ++j)
@@ -668,7 +486,9 @@ cudaError_t launch_cache8_attend(const Cache8& c, Tok8<const TQ> q, int slabs, s
 #define RLT_RUN(MODE, NB)                                                                       \
     (c.dh == 64 ? run<64, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)       \
                 : run<128, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st))
-    if (nq <= 4) return RLT_RUN(FOLD, 1);
+    if (nq <= 4)
+        return launch_cache8_decode<TQ, TO>(c, q, slabs, slab, out, heads, n, lens, lens_add, scale,
+                                            rope, st);
     if constexpr (std::is_same<TQ, bf16>::value && std::is_same<TO, bf16>::value)
         return nq <= 8 ? RLT_RUN(PLAIN, 1) : RLT_RUN(PLAIN, 2);
     else

@@ -1,0 +1,449 @@
+// Attention over the paged 8-bit cache for up to 4 query vectors per key head:
+// generated tokens (include/rlt.h: rlt_cache8_attend).
+//
+// Mathematics.  With byte values x, key scales ks and value scales vs per
+// (page, head), o = sum_j p_j vs_j x^v_j / sum_j p_j, p_j = 2^(s_j),
+// s_j = scale log2(e) ks_j q.x^k_j.  The value scale is folded into the
+// exponent: w_j = 2^(s_j + log2 vs_j - m) with m a running maximum of
+// s + log2 vs, so that o = sum w_j x^v_j / sum (w_j / vs_j): bytes enter the
+// two products as they are (e4m3 is exact in fp16), a 16-key tile needs two
+// scalars per head, and w stays within fp16's range whatever the scales.
+//
+// Matrix form.  One warp takes 16 keys at a time through m16n8k16 fp16
+// products with fp32 sums, keys (then value dims) as the 16 rows, queries as
+// the 8 columns: converting a byte pair to fp16 is one instruction where
+// multiplying it in fp32 on the CUDA cores would take four, so the tensor
+// cores carry the per-key work of an HBM stream even for one query.  Columns
+// 2i and 2i + 1 hold query i's (then weight i's) leading 11 bits and the next
+// 11 bits times 2^11: a lane meets both sums of a score, and adds them in
+// fp32.  The weights pass from the score product's layout to the value
+// product's operand by an 8x8 transpose of the warp's registers (movmatrix).
+// The maximum is raised only when a score passes it by 2^8 (one warp vote per
+// tile instead of a reduction); fp16 holds weights up to 2^16.
+//
+// Split.  A prefix is cut into runs of whole tiles: up to 16 of them of at
+// least 64 keys, twice as many for every doubling from 8192 keys on (256 at
+// most).  Every run's sums are kept apart and joined in run order, 16 runs at
+// a time in shared memory and then these groups through the cluster's
+// distributed shared memory: no scratch, no atomics, and the same bits for a
+// row whatever batch or capacity it sits in.  Who works on the runs is free:
+// a group's runs belong to 1 to 16 warps, as many as fill the machine, and a
+// warp's copies run on from one of its runs into the next.  Measured by the
+// launcher's comment.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "cache8_tile.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace rlt {
+namespace {
+
+constexpr int kGroupRuns = 16;          // runs joined in one CTA
+constexpr int kMinTiles = 4;            // of a run
+constexpr int kMaxGroups = 16;          // CTAs of a cluster
+constexpr size_t kMostSmem = 227 * 1024;
+constexpr int64_t kGroupKeys = 4096;    // keys per group, from two groups on
+
+template <int D> constexpr int stages() { return D == 64 ? 4 : 3; }
+template <int D> constexpr int stage_bytes() { return 2 * kTile * D + 16; }
+template <int D, int NW> constexpr int ring_bytes() { return NW * stages<D>() * stage_bytes<D>(); }
+
+__host__ __device__ __forceinline__ int groups_of(int64_t keys) {
+    int g = 1;
+    while (g < kMaxGroups && 2 * g * kGroupKeys <= keys) g *= 2;
+    return g;
+}
+// tiles of a run
+__host__ __device__ __forceinline__ int run_tiles(int tiles, int groups) {
+    const int len = (tiles + kGroupRuns * groups - 1) / (kGroupRuns * groups);
+    return len > kMinTiles ? len : kMinTiles;
+}
+
+// D = 64: 8 warps in 80 registers, three CTAs an SM; D = 128: two.  16 warps: one
+template <int D, int NW, typename TQ, typename TO>
+__global__ void __launch_bounds__(NW * 32, NW == 16 ? 1 : D == 64 ? 3 : 2)
+k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int units,
+                int unit_warps, int unit_runs, const int32_t* __restrict__ lens, int lens_add,
+                float scale_log2e, Rope8 rope) {
+    constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_enter();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nq = n * share;
+    // unit (row, key head) of this warp, and the warp's place among the unit's
+    const int here = warp / unit_warps, wi = warp - here * unit_warps;
+    const int64_t unit = (int64_t)(blockIdx.x / (unsigned)C) * (NW / unit_warps) + here;
+    const bool alive = unit < units;
+    const int row = alive ? (int)unit / c.kv_heads : 0, kvh = alive ? (int)unit % c.kv_heads : 0;
+
+    const int cap = c.row_pages << page_log2;
+    const int L0 = __ldg(lens + row) + lens_add;
+    const int L = max(0, min(cap, L0));
+    if ((L0 < 0 || L0 > cap) && alive && lane == 0 && wi == 0 && kvh == 0 && rank == 0 && c.status)
+        atomicCAS(c.status, 0, c.cap_code);
+    const int keys = alive ? L : 0;                 // the last query sees all, the first:
+    const int vis_min = L - n + 1;
+    const int tiles = (keys + kTile - 1) / kTile, groups = groups_of(keys);
+    if (rank >= groups) return;                     // (one unit per CTA then)
+    const int len = run_tiles(tiles, groups), runs = (tiles + len - 1) / len;
+    const int run0 = rank * kGroupRuns, run1 = min(runs, run0 + kGroupRuns);    // of this CTA
+    const int per = (run1 - run0 + unit_warps - 1) / unit_warps;
+    const int r_begin = min(run1, run0 + wi * per), r_end = min(run1, r_begin + per);
+    const int s_begin = r_begin * len, s_end = min(tiles, r_end * len);
+    // shared memory: the warps' tiles; per unit the queries (later the group's sums), its runs'
+    // O [run][query][D], m and l (padded to whole 16 bytes)
+    float* const s_unit = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
+                          here * (1 + unit_runs) * nq * (D + 4);
+    float* const s_o = s_unit + nq * (D + 4);
+    float* const s_m = s_o + unit_runs * nq * D;
+    float* const s_l = s_m + unit_runs * nq;
+
+    // ---------------------------------------------------------------- tiles
+    uint8_t* ring = smem + warp * (NST * SB);
+    const uint32_t ring_u = tc::smem_u32(ring);
+    const size_t head_bytes = (size_t)D << page_log2;
+    const size_t v_bytes = (size_t)c.kv_heads * head_bytes;
+    const uint8_t* const pages = c.pages + (size_t)kvh * head_bytes + lane * 16;
+    int b_base = s_begin;                   // first tile of the batch below
+    int b_page = -1;                        // lane l: the page of tile b_base + l, and its scalars
+    float b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
+    auto load_batch = [&]() {
+        b_page = -1;
+        b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
+        const int s = b_base + lane;
+        if (s < s_end) {
+            const int p = __ldg(c.table + (size_t)row * c.row_pages + ((s * kTile) >> page_log2));
+            if (p >= 0 && p < c.n_pages) {
+                const float* sc = c.scales + (size_t)p * 2 * c.kv_heads + kvh;
+                b_page = p;
+                b_ks = __ldg(sc);
+                const float vs = __ldg(sc + c.kv_heads);
+                b_lv = log2f(vs);
+                b_inv = 1.f / vs;
+            } else if (c.status) {
+                atomicCAS(c.status, 0, c.arg_code);
+            }
+        }
+    };
+    const TileCopy<D> copy(lane);
+    int fs = s_begin, fslot = 0;            // the tile fetched next, and its stage
+    auto fetch = [&]() {
+        if (fs < s_end) {
+            if (fs - b_base == 32) {
+                b_base += 32;
+                load_batch();
+            }
+            const int src = fs - b_base;
+            const int p = __shfl_sync(0xffffffffu, b_page, src);
+            const float ks = __shfl_sync(0xffffffffu, b_ks, src);
+            const float lv = __shfl_sync(0xffffffffu, b_lv, src);
+            const float inv = __shfl_sync(0xffffffffu, b_inv, src);
+            if (lane == 0)
+                *reinterpret_cast<float4*>(ring + fslot * SB + 2 * kTile * D) =
+                    make_float4(ks, lv, inv, 0.f);
+            const int k0 = fs * kTile;
+            const uint8_t* kg = pages + (size_t)max(p, 0) * 2 * v_bytes +
+                                (size_t)((k0 & ((1 << page_log2) - 1)) * D);
+            copy(ring_u + fslot * SB, kg, kg + v_bytes, p >= 0 ? keys - k0 : 0, c.pages);
+        }
+        cp_commit();
+        ++fs;
+        fslot = fslot + 1 == NST ? 0 : fslot + 1;
+    };
+    load_batch();
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) fetch();
+
+    // ---------------------------------------------------------------- queries
+    // rotated once per unit, then split into operands by every warp
+    for (int x = wi * 32 + lane; x < nq * (D / 4); x += unit_warps * 32) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        const int i = r / share, pos = L - n + i + rope.origin;
+        const bool seen = alive && L - n + i >= 0;
+        const bool lost = seen && rope.rot && (pos < 0 || pos >= rope.positions);
+        if (lost && d == 0 && c.status) atomicCAS(c.status, 0, c.cap_code);
+        if (seen && !lost) {
+            const size_t at = (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
+                              (size_t)(kvh * share + r % share) * D;
+            load_q4(q, at, d, rope, pos, y);
+        }
+        *reinterpret_cast<float4*>(s_unit + r * (D + 4) + d) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    // column g: query g/2, this lane's dims [t D/4, (t+1) D/4) of it, leading or trailing bits
+    uint32_t qf[KI][2];
+    float rf = 0.f;                         // score factor of query t: 2^e scale log2(e)
+    int vis = 0;                            // keys it sees
+    {
+        const int r = g >> 1;
+        const float* sq = s_unit + r * (D + 4) + t * (D / 4);
+        float amax = 0.f;
+        if (r < nq)
+#pragma unroll
+            for (int k = 0; k < KI; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
+                amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+            }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // bring the query near 1 by a power of two (exact); 2^+-100 keeps both factors finite
+        int e2 = (int)(__float_as_uint(amax) >> 23) - 127;
+        e2 = max(-100, min(100, e2));
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
+#pragma unroll
+        for (int k = 0; k < KI; ++k) {
+            qf[k][0] = qf[k][1] = 0u;
+            if (r < nq) {
+                const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
+                const float x0 = x.x * down, x1 = x.y * down, x2 = x.z * down, x3 = x.w * down;
+                const uint32_t h0 = pack_h2(x0, x1), h1 = pack_h2(x2, x3);
+                qf[k][0] = g & 1 ? rest_h2(x0, x1, h0) : h0;
+                qf[k][1] = g & 1 ? rest_h2(x2, x3, h1) : h1;
+            }
+        }
+        rf = __shfl_sync(0xffffffffu, up, 8 * t);
+        const int i = t / share, pos = L - n + i + rope.origin;
+        vis = t < nq ? max(0, L - n + i + 1) : 0;
+        if (rope.rot && (pos < 0 || pos >= rope.positions)) vis = 0;
+    }
+    // a query without a rotation sees nothing: its column has to be masked from the first key on
+    const int mask_from = __any_sync(0xffffffffu, t < nq && vis < vis_min) ? 0 : vis_min;
+
+    // ---------------------------------------------------------------- the runs
+    float m = -INFINITY, l = 0.f, O[VJ][4];
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
+    const int key_lo = 4 * (g & 1) + (g >> 1);      // sigma(g): the key of row g; row g + 8: + 8
+    int slot = 0, run = r_begin, run_left = len;
+
+    for (int s = s_begin; s < s_end; ++s) {
+        cp_wait<NST - 2>();
+        __syncwarp();                       // the tile is here; every lane has left the last one
+        fetch();
+        const uint8_t* st = ring + slot * SB;
+        slot = slot + 1 == NST ? 0 : slot + 1;
+        const float4 meta = *reinterpret_cast<const float4*>(st + 2 * kTile * D);
+        const int k0 = s * kTile;
+
+        float cf[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+            uint4 x, y;
+            load_keys<D>(st, g, t, h, x, y);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a[4];
+                h2x2_of(xs[k], a[0], a[2]);
+                h2x2_of(ys[k], a[1], a[3]);
+                mma_f16(cf, a, qf[4 * h + k][0], qf[4 * h + k][1]);
+            }
+        }
+        uint32_t vv[4][D / 32];
+        load_values<D>(st, g, t, vv);
+        // scores of key rows g, g + 8 and query t, the value scale folded in
+        const float f = rf * meta.x;
+        float s0 = fmaf(fmaf(cf[1], 1.f / 2048.f, cf[0]), f, meta.y);
+        float s1 = fmaf(fmaf(cf[3], 1.f / 2048.f, cf[2]), f, meta.y);
+        const bool bad = !(meta.y > -INFINITY);
+        uint32_t poison = 0;                // keys of the tile with a NaN among their values
+        if (bad || k0 + kTile > mask_from) {    // the prefix ends in this tile for some query
+            if (bad || k0 + key_lo >= vis) s0 = -INFINITY;
+            if (bad || k0 + key_lo + 8 >= vis) s1 = -INFINITY;
+            if (mask_from < keys) poison = clear_nan<D>(vv, t);
+        }
+        float mx = fmaxf(s0, s1);
+        if (__any_sync(0xffffffffu, mx > m + kLag)) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mn = fmaxf(m, mx);
+            const float r = m == mn ? 1.f : ex2(m - mn);        // m = -inf: 0
+            m = mn;
+            l *= r;
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) O[j][0] *= r, O[j][1] *= r, O[j][2] *= r, O[j][3] *= r;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float p0 = ex2(s0 - mm), p1 = ex2(s1 - mm);
+        if (poison) {
+            if (s0 != -INFINITY && ((poison >> key_lo) & 1u)) p0 = NAN;
+            if (s1 != -INFINITY && ((poison >> (key_lo + 8)) & 1u)) p1 = NAN;
+        }
+        l = fmaf(p0 + p1, meta.z, l);
+        // the value product's operand: column 2t the leading bits, 2t + 1 the rest
+        const float h0 = __half2float(__float2half_rn(p0)), h1 = __half2float(__float2half_rn(p1));
+        const uint32_t b0 = transpose8(pack_h2(h0, (p0 - h0) * 2048.f));
+        const uint32_t b1 = transpose8(pack_h2(h1, (p1 - h1) * 2048.f));
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            // bytes of the four values paired (key 0, key 1) and (key 2, key 3): bytes 0, 1 and
+            // 2, 3 of word x are dims 4x .. 4x+3 of this lane
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                h2x2_of(__byte_perm(vv[0][x], vv[1][x], y ? 0x7362 : 0x5140), a[0], a[1]);
+                h2x2_of(__byte_perm(vv[2][x], vv[3][x], y ? 0x7362 : 0x5140), a[2], a[3]);
+                mma_f16(O[2 * x + y], a, b0, b1);
+            }
+        }
+        if (--run_left == 0 || s + 1 == s_end) {        // the run's sums leave the registers
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (t < nq) {
+                const int at = (run - run0) * nq + t;
+                float* o = s_o + at * D + g * (D / 8);
+#pragma unroll
+                for (int j = 0; j < VJ; ++j)
+                    *reinterpret_cast<float2*>(o + 2 * j) =
+                        make_float2(fmaf(O[j][1], 1.f / 2048.f, O[j][0]),
+                                    fmaf(O[j][3], 1.f / 2048.f, O[j][2]));
+                if (g == 0) s_m[at] = m, s_l[at] = l;
+            }
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
+            m = -INFINITY, l = 0.f;
+            ++run;
+            run_left = len;
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // ---------------------------------------------------------------- join
+    auto put = [&](int r, int d, float o, float lsum) {
+        out.p[(int64_t)row * out.row + (int64_t)(r / share) * out.token +
+              (int64_t)(kvh * share + r % share) * D + d] =
+            from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
+    };
+    float* const g_m = s_unit + nq * D;             // the group's sums: O [query][D], m, l
+    float* const g_l = g_m + nq;
+    const int mine = run1 - run0;                   // (fewer than 0: none)
+    if (alive)
+        for (int x = wi * 32 + lane; x < nq * D; x += unit_warps * 32) {
+            const int r = x / D, d = x % D;
+            float M = -INFINITY;
+            for (int k = 0; k < mine; ++k) M = fmaxf(M, s_m[k * nq + r]);
+            float o = 0.f, ls = 0.f;
+            for (int k = 0; k < mine; ++k) {
+                const float mk = s_m[k * nq + r];
+                const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
+                o = fmaf(f, s_o[k * nq * D + x], o);
+                ls = fmaf(f, s_l[k * nq + r], ls);
+            }
+            if (groups == 1) {
+                put(r, d, o, ls);
+            } else {
+                s_unit[x] = o;
+                if (d == 0) g_m[r] = M, g_l[r] = ls;
+            }
+        }
+    if (groups == 1) return;
+    cluster.sync();                                 // (CTAs without a group have exited)
+    for (int x = rank * NW * 32 + (int)threadIdx.x; x < nq * D; x += groups * NW * 32) {
+        const int r = x / D, d = x % D;
+        float M = -INFINITY;
+        for (int k = 0; k < groups; ++k) M = fmaxf(M, *cluster.map_shared_rank(g_m + r, k));
+        float o = 0.f, ls = 0.f;
+        for (int k = 0; k < groups; ++k) {
+            const float mk = *cluster.map_shared_rank(g_m + r, k);
+            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
+            o = fmaf(f, *cluster.map_shared_rank(s_unit + x, k), o);
+            ls = fmaf(f, *cluster.map_shared_rank(g_l + r, k), ls);
+        }
+        put(r, d, o, ls);
+    }
+    cluster.sync();                                 // no CTA leaves while its memory is read
+}
+
+template <int D, int NW, typename TQ, typename TO>
+cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int share, int n,
+                const int32_t* lens, int lens_add, float scale, const Rope8& rope, int64_t units,
+                int C, int unit_warps, int unit_runs, size_t smem, cudaStream_t st) {
+    auto* kern = k_cache8_decode<D, NW, TQ, TO>;
+    const void* kp = reinterpret_cast<const void*>(kern);
+    int page_log2 = 4;
+    while ((1 << page_log2) < c.page) ++page_log2;
+    const int per_cta = NW / unit_warps;
+    const int64_t ctas = (units + per_cta - 1) / per_cta * C;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (smem > kMostSmem || !set_smem_once(kp, kMostSmem) || (C > 8 && !set_wide_cluster_once(kp)))
+        return cudaErrorInvalidConfiguration;
+    set_carveout_once(kp);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    const float scale_log2e = (float)((double)scale * 1.4426950408889634);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, c, page_log2, q, out, share, n, (int)units,
+                                       unit_warps, unit_runs, lens, lens_add, scale_log2e, rope);
+    if (e == cudaSuccess) rlt_count_launch();
+    return e;
+}
+
+template <int D, typename TQ, typename TO>
+cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int share, int n,
+                 const int32_t* lens, int lens_add, float scale, const Rope8& rope,
+                 cudaStream_t st) {
+    const int64_t cap = (int64_t)c.row_pages * c.page, units = (int64_t)c.rows * c.kv_heads;
+    if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const int C = groups_of(cap), nq = n * share;
+    // runs that a group of a prefix up to the capacity can have: 16, or one per 64 keys
+    const int unit_runs = (int)std::min<int64_t>(kGroupRuns, (cap / kTile + kMinTiles - 1) / kMinTiles);
+    auto smem = [&](int nw, int w) {
+        const int ring = nw == 16 ? ring_bytes<D, 16>() : ring_bytes<D, 8>();
+        return (size_t)ring + (size_t)(nw / w) * (1 + unit_runs) * nq * (D + 4) * 4;
+    };
+    // Warps of a unit: 16 where a few units are all there is and the sums fit beside their tiles;
+    // else as many as fill the machine (16 an SM), as long as the runs' sums leave room for as
+    // many CTAs.
+    const int64_t fill = 148 * 16;
+    if (unit_runs > 8 && units * C * 8 < fill && smem(16, 16) <= kMostSmem)
+        return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, 16, unit_runs,
+                          smem(16, 16), st);
+    int w = 8;
+    if (C == 1)
+        while (w > 1 && (units * (w / 2) >= fill || w / 2 >= unit_runs) &&
+               smem(8, w / 2) <= (D == 64 ? 74 : 112) * 1024)
+            w /= 2;
+    return run<D, 8>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, w, unit_runs,
+                     smem(8, w), st);
+}
+
+}  // namespace
+
+template <typename TQ, typename TO>
+cudaError_t launch_cache8_decode(const Cache8& c, Tok8<const TQ> q, int slabs, size_t slab,
+                                 Tok8<TO> out, int heads, int n, const int32_t* lens,
+                                 int lens_add, float scale, const Rope8& rope, cudaStream_t st) {
+    const QIn<TQ> qi{q.p, q.row, q.token, slabs, slab};
+    const int share = heads / c.kv_heads;
+    return c.dh == 64 ? plan<64>(c, qi, out, share, n, lens, lens_add, scale, rope, st)
+                      : plan<128>(c, qi, out, share, n, lens, lens_add, scale, rope, st);
+}
+
+#define RLT_INST(TQ, TO)                                                                         \
+    template cudaError_t launch_cache8_decode<TQ, TO>(const Cache8&, Tok8<const TQ>, int, size_t, \
+                                                      Tok8<TO>, int, int, const int32_t*, int,   \
+                                                      float, const Rope8&, cudaStream_t);
+RLT_INST(float, float)
+RLT_INST(bf16, bf16)
+RLT_INST(float, bf16)
+#undef RLT_INST
+
+}  // namespace rlt
