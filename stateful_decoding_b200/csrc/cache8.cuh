@@ -11,7 +11,8 @@ struct Cache8 {
     float* scales;            // [n_pages][2][kv_heads]
     const int32_t* table;     // [rows][row_pages]
     int* status;              // sticky word, may be null
-    int arg_code, cap_code;   // what it is set to: bad table entry; bad length or position
+    // what it is set to: bad table entry; bad length or position; a bounded wait gave up
+    int arg_code, cap_code, late_code;
     int n_pages, rows, row_pages, page, kv_heads, dh;
 };
 

@@ -1,6 +1,7 @@
 // Pieces that the kernels of attention over the paged 8-bit cache share.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -89,34 +90,48 @@ __device__ __forceinline__ void load4(const QIn<bf16>& q, size_t at, float (&x)[
     x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-// dims d..d+3 (d a multiple of 4) of the query at `at`, rotated at position pos
+// Dims d..d+3 (d a multiple of 4) of a query, rotated at its position: loads and arithmetic apart,
+// so that the loads' latency overlaps what stands between.
 template <typename TQ>
-__device__ __forceinline__ void load_q4(const QIn<TQ>& q, size_t at, int d, const Rope8& r, int pos,
-                                        float (&x)[4]) {
-    load4(q, at + d, x);
-    if (d >= r.rot) return;
-    const int half = r.rot >> 1;
-    const float* cs = r.cs + (size_t)pos * half;
-    const float* sn = r.sn + (size_t)pos * half;
-    if (r.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float c = __ldg(cs + d / 2 + e), s = __ldg(sn + d / 2 + e);
-            rope_pair(x[2 * e], x[2 * e + 1], c, s, x[2 * e], x[2 * e + 1]);
-        }
-    } else {
-        const bool low = d < half;
-        const int a = low ? d : d - half;
-        float y[4], unused;
-        load4(q, at + (low ? d + half : d - half), y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float c = __ldg(cs + a + e), s = __ldg(sn + a + e);
-            if (low) rope_pair(x[e], y[e], c, s, x[e], unused);
-            else rope_pair(y[e], x[e], c, s, unused, x[e]);
+struct Q4 {
+    float x[4], y[4], c[4], s[4];           // the dims, their partners, cosines and sines
+    __device__ __forceinline__ void load(const QIn<TQ>& q, size_t at, int d, const Rope8& r, int pos) {
+        load4(q, at + d, x);
+        if (d >= r.rot) return;
+        const int half = r.rot >> 1;
+        const size_t row = (size_t)pos * half;
+        if (r.interleaved) {
+            const float2 a = __ldg(reinterpret_cast<const float2*>(r.cs + row + d / 2));
+            const float2 b = __ldg(reinterpret_cast<const float2*>(r.sn + row + d / 2));
+            c[0] = a.x, c[1] = a.y, s[0] = b.x, s[1] = b.y;
+        } else {
+            const bool low = d < half;
+            load4(q, at + (low ? d + half : d - half), y);
+            const size_t from = row + (low ? d : d - half);
+            const float4 a = __ldg(reinterpret_cast<const float4*>(r.cs + from));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(r.sn + from));
+            c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+            s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
         }
     }
-}
+    __device__ __forceinline__ float4 turned(int d, const Rope8& r) {
+        if (d < r.rot) {
+            if (r.interleaved) {
+                rope_pair(x[0], x[1], c[0], s[0], x[0], x[1]);
+                rope_pair(x[2], x[3], c[1], s[1], x[2], x[3]);
+            } else {
+                const bool low = d < (r.rot >> 1);
+                float unused;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (low) rope_pair(x[e], y[e], c[e], s[e], x[e], unused);
+                    else rope_pair(y[e], x[e], c[e], s[e], unused, x[e]);
+                }
+            }
+        }
+        return make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
 
 // Where a lane's pieces of a 16-key tile go in shared memory (K rows, then V rows): key rows and
 // 16-byte chunks are permuted on the way in so that every fragment load is one conflict-free wide
@@ -197,6 +212,50 @@ __device__ __forceinline__ uint32_t clear_nan(uint32_t (&vv)[4][D / 32], int t) 
         if (hit) poison |= 1u << (4 * i + t);
     }
     return __reduce_or_sync(0xffffffffu, poison);
+}
+
+// The CTAs' sums in a cluster's shared memory (O [query][D], m and l at the same places in each)
+// as one, in CTA order: this CTA's share of the outputs goes to put(query, dim, o, l).  `scratch`
+// holds 3 x 16 floats a query.  Every remote load of a thread is in flight at once: one after
+// another, 16 CTAs took 12 us.
+template <int D, typename Put>
+__device__ __forceinline__ void join_cluster(const cooperative_groups::cluster_group& cluster,
+                                             int ctas, int rank, int threads, int queries,
+                                             float* o_at, float* m_at, float* l_at, float* scratch,
+                                             Put put) {
+    constexpr int MOST = 16;
+    float* const s_m = scratch;             // [cta][query]: m, later its factor
+    float* const s_l = scratch + MOST * queries;
+    float* const s_sum = s_l + MOST * queries;
+    for (int x = threadIdx.x; x < ctas * queries; x += threads) {
+        const int k = x / queries, r = x - k * queries;
+        s_m[x] = *cluster.map_shared_rank(m_at + r, k);
+        s_l[x] = *cluster.map_shared_rank(l_at + r, k);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < queries; r += threads) {
+        float M = -INFINITY, ls = 0.f;
+        for (int k = 0; k < ctas; ++k) M = fmaxf(M, s_m[k * queries + r]);
+        for (int k = 0; k < ctas; ++k) {
+            const float mk = s_m[k * queries + r];
+            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
+            s_m[k * queries + r] = f;
+            ls = fmaf(f, s_l[k * queries + r], ls);
+        }
+        s_sum[r] = ls;
+    }
+    __syncthreads();
+    for (int x = rank * threads + (int)threadIdx.x; x < queries * D; x += ctas * threads) {
+        const int r = x / D;
+        float v[MOST];
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) v[k] = k < ctas ? *cluster.map_shared_rank(o_at + x, k) : 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int k = 0; k < MOST; ++k)
+            if (k < ctas) o = fmaf(s_m[k * queries + r], v[k], o);
+        put(r, x - r * D, o, s_sum[r]);
+    }
 }
 
 }  // namespace

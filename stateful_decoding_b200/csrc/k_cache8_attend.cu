@@ -1,51 +1,42 @@
-// Attention over the paged 8-bit cache (include/rlt.h: rlt_cache8_attend).
+// Attention over the paged 8-bit cache for 5 and more query vectors per key
+// head: blocks of tokens, shared key heads (include/rlt.h: rlt_cache8_attend).
 //
-// Mathematics.  With byte values x, key scales ks and value scales vs per
-// (page, head), o = sum_j p_j vs_j x^v_j / sum_j p_j, p_j = 2^(s_j),
-// s_j = scale log2(e) ks_j q.x^k_j.  The value scale is folded into the
-// exponent: w_j = 2^(s_j + log2 vs_j - m) with m a running maximum of
-// s + log2 vs, so that o = sum w_j x^v_j / sum (w_j / vs_j): bytes enter the
-// two products as they are (e4m3 is exact in fp16), a 16-key tile needs two
-// scalars per head, and w stays within fp16's range whatever the scales.
+// Mathematics, as for fewer queries (k_cache8_decode.cu): the value scale goes
+// into the exponent, so bytes enter both products as they are.  Here a CTA
+// takes 128 keys at a time through the fifth-generation tensor cores, keys as
+// the rows of the first product and value dims as those of the second:
+//   S [128 keys][N]  = K [128][D] . Q^T       (K and Q row by row)
+//   O [128 dims][N] += V^T [D][128] . w       (V and w as they lie, key by key)
+// Both accumulators live in tensor memory.  One CTA an SM, three kinds of
+// warps, two tiles of everything in turn:
+//   8 convert  16 keys each: e4m3 bytes become fp16 (exactly) on their way
+//              from registers, where the next tile's bytes arrive (the one
+//              after is on its way to L2), to swizzled shared memory; one layout
+//              [dims/64][key][64 dims] serves K, read along the dims, and V,
+//              read across them;
+//   1 issues   the products: tile i + 1's first one before tile i's second;
+//   8 weigh    a thread of the first (second) four has one key and the first
+//              (second) half of the columns: weights need no exchange between
+//              lanes, and any number of queries keeps all lanes busy.
 //
-// Matrix form.  One warp takes 16 keys at a time through m16n8k16 fp16
-// products with fp32 sums, keys (then value dims) as the 16 rows, queries as
-// the 8 columns: converting a byte pair to fp16 is one instruction where
-// multiplying it in fp32 on the CUDA cores would take four, so the tensor
-// cores carry the per-key work of an HBM stream even for one query.  (Queries
-// as rows, tried first, need twice the products and twice the registers of
-// the output: 618 instructions per 4 KB tile and 12 warps an SM, 2.5 TB/s on 64
-// rows x 16 heads x 4.3k keys.)  Columns left over buy precision:
-//   FOLD   up to 4 query vectors per key head: columns 0-3 hold the leading 11
-//          bits of q (of w), columns 4-7 the next 11 bits times 2^11, and the two
-//          sums are added in fp32;
-//   SPLIT  up to 8, fp32 types: the same in two products;
-//   PLAIN  8 or 16 bf16 queries, leading bits alone: a bf16 q is exact there
-//          (each query is brought near 1 by a power of two first), w is rounded
-//          to fp16 (2^-11 relative at most, below the bf16 output's 2^-9 step).
-// The weights pass from the score product's layout to the value product's
-// operand by an 8x8 transpose of the warp's registers (movmatrix).
+// PARTS = 2 (fp32 types): columns 2i and 2i + 1 hold query i's (weight i's)
+// leading 11 bits and the next 11 bits times 2^11, added in fp32.  PARTS = 1
+// (bf16 types): leading bits alone.  Each query is brought near 1 by a power
+// of two first: a bf16 query is exact then, a rotated one is rounded to fp16
+// (half a step 2^-12), as weights are: below the bf16 output's 2^-9.
 //
-// The maximum is raised only when a score passes it by 2^8 (one warp vote per
-// tile instead of a reduction); fp16 holds weights up to 2^16.
+// The maximum of a query is raised only when a score passes it by 2^8 (one
+// barrier vote per tile); then the columns' maxima are found and O rescaled.
 //
-// Data path.  Tiles reach a per-warp ring in shared memory by 16-byte
-// cp.async copies; keys past the prefix and keys in bad pages are zero-filled
-// rather than read, so whatever bytes sit there never enter a product.  Key
-// rows and 16-byte chunks are permuted on the way in so that every fragment
-// load is one conflict-free wide load: lane (g, t) = (lane/4, lane%4) reads
-// dims [t D/4, (t+1) D/4) of key rows g and g + 8 and of query g, and dims
-// [g D/8, (g+1) D/8) of values 4i + t; key row r holds key
-// sigma(r) = (r & 8) + 4 (r & 1) + (r & 7) / 2, the order the transpose wants.
-//
-// Split.  The prefix of a (row, key head) is cut into runs for 4 warps of
-// 2^j <= keys / 1024 CTAs (1 to 16), a function of that prefix alone.  The
-// warps' partial results meet in shared memory, the CTAs' through the
-// cluster's distributed shared memory, always in run order: no scratch, no
-// atomics, and the same bits for a row whatever batch or capacity it sits in.
+// Split.  The prefix of a (row, key head) is cut into runs of 2048 keys, or 8
+// longer ones (16 from 32768 keys on), for a CTA each, a function of that
+// prefix alone; they join through the cluster's distributed shared memory in
+// run order: no scratch, no atomics, and the same bits for a row whatever batch
+// or capacity it sits in.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+
 #include "cache8_tile.cuh"
 
 namespace cg = cooperative_groups;
@@ -53,411 +44,601 @@ namespace cg = cooperative_groups;
 namespace rlt {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kKeysPerCta = 1024;
-constexpr int kMaxCtas = 16;            // CTAs per (row, key head, query tile): one cluster
+constexpr int kWarps = 8, kConvert = 8;     // that weigh; that convert; one more issues
+constexpr int kWeigh = 32 * kWarps, kThreads = 32 * (kWarps + kConvert + 1);
+constexpr int kKeys = 128;              // of a tile
+constexpr int kKeysPerCta = 2048;
+constexpr int64_t kLongKeys = 32768;    // from here on
+constexpr int kMaxCtas = 16;            // CTAs (one cluster) share a prefix, below
+constexpr int kFewCtas = 8;             // (clusters of 16 leave a quarter of the SMs idle)
+constexpr float kNone = -3e38f;         // below every finite score
+constexpr uint32_t kAtom = kKeys * 128; // 64 dims of 128 keys in fp16
 
-template <int D> constexpr int stages() { return D == 64 ? 4 : 3; }
-template <int D> constexpr int stage_bytes() { return 2 * kTile * D + 16; }
-template <int D> constexpr int ring_bytes() { return kWarps * stages<D>() * stage_bytes<D>(); }
-
-enum Mode { SPLIT, PLAIN };
-constexpr int queries_of(int mode, int nb) { return mode == SPLIT ? 8 : 8 * nb; }
-
-// CTAs that share a prefix of `keys` keys: a power of two, kKeysPerCta keys each at least
+// CTAs that share a prefix of `keys` keys: of kKeysPerCta keys each, then of more
 __host__ __device__ __forceinline__ int ctas_of(int64_t keys) {
-    int c = 1;
-    while (c < kMaxCtas && (int64_t)c * 2 * kKeysPerCta <= keys) c *= 2;
-    return c;
+    const int64_t c = (keys + kKeysPerCta - 1) / kKeysPerCta;
+    const int most = keys >= kLongKeys ? kMaxCtas : kFewCtas;
+    return c < 1 ? 1 : c > most ? most : (int)c;
+}
+// Instruction descriptor: fp16 A and B, fp32 accumulator, M = 128; mn: both operands are stored
+// along M and N rather than K.
+constexpr uint32_t idesc_f16(int N, bool mn) {
+    return (1u << 4) | (mn ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Shared-memory descriptor, 128-byte swizzle, stored along M (or N): 64 of them by 8 of K make an
+// atom; atoms follow each other along K every 1024 bytes (SBO), along M every kAtom (LBO).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kAtom >> 4) << 16) | (64ull << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float* v) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])));
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t key_of(float x) {   // order-preserving
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// MODE and NB (products of 8 columns): SPLIT 2, PLAIN 1 or 2
-template <int D, int MODE, int NB, typename TQ, typename TO>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D, int N>
+constexpr size_t smem_of() {
+    return 1024 + (size_t)(D / 64) * (4 * kAtom + N * 128) + 2 * kAtom;
+}
+
+// N columns of PARTS a query
+template <int D, int N, int PARTS, typename TQ, typename TO>
+__global__ void __launch_bounds__(kThreads, 1)
 k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int q_tiles,
                 const int32_t* __restrict__ lens, int lens_add, float scale_log2e, Rope8 rope) {
-    constexpr int QT = queries_of(MODE, NB);    // query vectors per tile
-    constexpr int NS = MODE == PLAIN ? NB : 1;  // column tiles of scores: queries 8 b + 2t + e
-    constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) float s_q[QT][D + 4];
+    constexpr int QT = N / PARTS;               // query vectors of a tile
+    constexpr int NC = N / 2, NQ = QT / 2;      // a thread's columns, and queries
+    constexpr int NL = D / 32;                  // a thread's 16-byte loads of K (and of V) per tile
+    constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (3 N used)
+    extern __shared__ uint8_t raw[];
+    // per query: score factor; maximum (0 before the first score); how far a score may pass it
+    // (kNone before the first score); the last rise of the maximum, and what it leaves of the sums
+    __shared__ __align__(16) float s_rf[QT], s_m[QT], s_lag[QT], s_up[QT], s_f[QT];
+    __shared__ __align__(16) int s_vis[QT];
+    __shared__ int64_t s_out[QT];               // where its output goes
+    __shared__ float4 s_meta[2][kKeys / 16];        // per 16 keys: ks, log2 vs, 1 / vs
+    __shared__ uint32_t s_poison[2][kKeys / 16];    // per 16 keys: those with a NaN value
+    __shared__ float s_red[4][QT];
+    __shared__ __align__(8) uint64_t s_k[2], s_v[2], s_s[2], s_w[2], s_o[2];   // K, V, S, w there; O done
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Before the next kernel of the stream may start: it could take the tensor memory that this
+    // CTA needs and then wait for this grid.
+    if (warp == 0) tc::tmem_alloc(&s_tmem, kCols);
+    if (tid == 0) {
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&s_k[b], kConvert);
+            tc::mbar_init(&s_v[b], kConvert);
+            tc::mbar_init(&s_s[b], 1);
+            tc::mbar_init(&s_w[b], kWarps);
+            tc::mbar_init(&s_o[b], 1);
+        }
+        s_abort = 0;
+        tc::fence_mbar_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int unit = (int)(blockIdx.x / (unsigned)C);
     const int mt = unit % q_tiles, bh = unit / q_tiles;
     const int kvh = bh % c.kv_heads, row = bh / c.kv_heads;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nq = n * share;
 
     const int cap = c.row_pages << page_log2;
     const int L0 = __ldg(lens + row) + lens_add;
     const int L = max(0, min(cap, L0));
-    if ((L0 < 0 || L0 > cap) && threadIdx.x == 0 && kvh == 0 && mt == 0 && rank == 0 && c.status)
-        atomicCAS(c.status, 0, c.cap_code);
+    auto say = [&](int code) {
+        if (c.status) atomicCAS(c.status, 0, code);
+    };
+    if ((L0 < 0 || L0 > cap) && tid == 0 && kvh == 0 && mt == 0 && rank == 0) say(c.cap_code);
     const int r0 = mt * QT, live = min(QT, nq - r0);
-    const int vis_max = max(0, L - n + (r0 + live - 1) / share + 1);  // keys any query of the tile sees
-    const int vis_min = L - n + r0 / share + 1;                      // keys all of them see
-    const int nC = min(C, ctas_of(vis_max));
-    if (rank >= nC) return;
-    const int subs = (vis_max + kTile - 1) / kTile, runs = nC * kWarps;
-    const int per = (subs + runs - 1) / runs;
-    const int s_begin = min(subs, (rank * kWarps + warp) * per), s_end = min(subs, s_begin + per);
+    const int keys = max(0, L - n + (r0 + live - 1) / share + 1);   // any query of the tile sees
+    const int vis_min = L - n + r0 / share + 1;                     // all of them see
+    const int nC = min(C, ctas_of(keys));
+    if (rank >= nC) {
+        if (warp == 0) tc::tmem_dealloc(tmem, kCols);
+        return;
+    }
+    const int tiles = (keys + kKeys - 1) / kKeys, per = (tiles + nC - 1) / nC;
+    const int t_begin = min(tiles, rank * per), t_end = min(tiles, t_begin + per);
 
-    // ---------------------------------------------------------------- tiles
-    uint8_t* ring = smem + warp * (NST * SB);
-    const uint32_t ring_u = tc::smem_u32(ring);
+    uint8_t* const base = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    constexpr uint32_t KV = (D / 64) * kAtom;
+    uint8_t* const K16 = base;                              // 2 x [D/64][key][64 dims]
+    uint8_t* const V16 = K16 + 2 * KV;
+    uint8_t* const W16 = V16 + 2 * KV;                      // 2 x weights [key][64 columns]
+    uint8_t* const Q16 = W16 + 2 * kAtom;                   // [D/64][column][64 dims]
+    // a bounded wait; once one gave up all do
+    auto wait = [&](uint64_t* bar, int i) {                 // for the barrier's use by tile i
+        for (uint32_t polls = 0; polls < (1u << 22); ++polls) {
+            if (tc::mbar_try(bar, (uint32_t)(i >> 1) & 1u)) return true;
+            if (*(volatile int*)&s_abort) return false;
+        }
+        *(volatile int*)&s_abort = 1;
+        return false;
+    };
+    auto arrive = [&](uint64_t* bar) {                      // the warp's writes are done
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
+
+    // ---------------------------------------------------------------- the next tile's bytes
+    // a converting warp copies 16 keys, which share a page: lane (r, ch) chunk ch (and ch + 4) of
+    // key r, r + 8
     const size_t head_bytes = (size_t)D << page_log2;
     const size_t v_bytes = (size_t)c.kv_heads * head_bytes;
-    int b_base = s_begin;                   // first tile of the batch below
-    int b_page = -1;                        // lane l: the page of tile b_base + l, and its scalars
-    float b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
-    auto load_batch = [&]() {
-        b_page = -1;
-        b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
-        const int s = b_base + lane;
-        if (s < s_end) {
-            const int p = __ldg(c.table + (size_t)row * c.row_pages + ((s * kTile) >> page_log2));
-            if (p >= 0 && p < c.n_pages) {
-                const float* sc = c.scales + (size_t)p * 2 * c.kv_heads + kvh;
-                b_page = p;
-                b_ks = __ldg(sc);
-                const float vs = __ldg(sc + c.kv_heads);
-                b_lv = log2f(vs);
-                b_inv = 1.f / vs;
-            } else if (c.status) {
-                atomicCAS(c.status, 0, c.arg_code);
-            }
-        }
+    const int lr = lane >> 2, lc = lane & 3;
+    const int cw = warp - kWarps;               // which of them
+    uint4 kb[NL], vb[NL];
+    float ks = 0.f, vs = 0.f;                   // vs = 0: no such keys
+    int page_1 = -1, page_2 = -1;               // of the tile loaded next, and of the one after
+    int entry = -1;                             // the table's, for the tile after that
+    auto entry_of = [&](int tile) {
+        const int k0 = tile * kKeys + cw * 16;
+        return tile < t_end && k0 < keys
+                   ? __ldg(c.table + (size_t)row * c.row_pages + (k0 >> page_log2)) : -1;
     };
-    const TileCopy<D> copy(lane);
-    auto issue = [&](int i) {               // tile s_begin + i into stage i % NST
-        const int s = s_begin + i;
-        if (s < s_end) {
-            if (s - b_base == 32) {
-                b_base += 32;
-                load_batch();
-            }
-            const int src = s - b_base;
-            const int p = __shfl_sync(0xffffffffu, b_page, src);
-            const float ks = __shfl_sync(0xffffffffu, b_ks, src);
-            const float lv = __shfl_sync(0xffffffffu, b_lv, src);
-            const float inv = __shfl_sync(0xffffffffu, b_inv, src);
-            const int slot = i % NST, k0 = s * kTile;
-            if (lane == 0)
-                *reinterpret_cast<float4*>(ring + slot * SB + 2 * kTile * D) =
-                    make_float4(ks, lv, inv, 0.f);
-            const uint8_t* kg = c.pages + ((size_t)max(p, 0) * 2 * c.kv_heads + kvh) * head_bytes +
-                                (size_t)(k0 & ((1 << page_log2) - 1)) * D + lane * 16;
-            copy(ring_u + slot * SB, kg, kg + v_bytes, p >= 0 ? vis_max - k0 : 0, c.pages);
-        }
-        cp_commit();
+    auto page_of = [&](int tile, int p) {       // -1: past the prefix, or bad
+        if (p >= 0 && p < c.n_pages) return p;
+        if (lane == 0 && tile < t_end && tile * kKeys + cw * 16 < keys) say(c.arg_code);
+        return -1;
     };
-    load_batch();
+    auto bytes_of = [&](int tile, int page) {
+        const int k0 = tile * kKeys + cw * 16;
+        return c.pages + ((size_t)max(page, 0) * 2 * c.kv_heads + kvh) * head_bytes +
+               (size_t)((k0 & ((1 << page_log2) - 1)) * D);
+    };
+    auto load_half = [&](int tile, bool values, uint4 (&b)[NL]) {
+        const int k0 = tile * kKeys + cw * 16;
+        const uint8_t* from = bytes_of(tile, page_1) + lr * D + lc * 16 + (values ? v_bytes : 0);
 #pragma unroll
-    for (int i = 0; i < NST - 1; ++i) issue(i);
-
-    // ---------------------------------------------------------------- queries
-    // rotated once per CTA, then split into operands by every warp
-    for (int x = threadIdx.x; x < QT * (D / 4); x += kWarps * 32) {
-        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < live) {
-            const int rr = r0 + r, i = rr / share, pos = L - n + i + rope.origin;
-            const bool seen = L - n + i >= 0;
-            const bool lost = seen && rope.rot && (pos < 0 || pos >= rope.positions);
-            if (lost && d == 0 && c.status) atomicCAS(c.status, 0, c.cap_code);
-            if (seen && !lost) {
-                const size_t at = (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
-                                  (size_t)(kvh * share + rr % share) * D;
-                load_q4(q, at, d, rope, pos, y);
-            }
+        for (int j = 0; j < NL; ++j) {
+            const int r8 = D == 128 ? j >> 1 : j, off = r8 * 8 * D + (D == 128 ? (j & 1) * 64 : 0);
+            const bool ok = page_1 >= 0 && k0 + lr + 8 * r8 < keys;
+            b[j] = ok ? __ldg(reinterpret_cast<const uint4*>(from + off)) : make_uint4(0, 0, 0, 0);
         }
-        *reinterpret_cast<float4*>(&s_q[r][d]) = make_float4(y[0], y[1], y[2], y[3]);
+    };
+    auto load_scales = [&]() {
+        vs = 0.f;
+        if (page_1 >= 0) {
+            const float* sc = c.scales + (size_t)page_1 * 2 * c.kv_heads + kvh;
+            ks = __ldg(sc);
+            vs = __ldg(sc + c.kv_heads);
+        }
+    };
+    auto ahead = [&](int tile) {                // 128 bytes a lane: K by the first half, then V
+        const int at = (lane & 15) * 128;
+        if (page_2 >= 0 && at < 16 * D) {
+            const uint8_t* p = bytes_of(tile, page_2) + at + (lane < 16 ? 0 : v_bytes);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        }
+    };
+    const bool converts = warp >= kWarps && warp < kWarps + kConvert;
+    if (converts) {
+        const int e0 = entry_of(t_begin), e1 = entry_of(t_begin + 1);
+        entry = entry_of(t_begin + 2);
+        page_1 = page_of(t_begin, e0);
+        load_scales();
+        load_half(t_begin, false, kb);
+        load_half(t_begin, true, vb);
+        page_2 = page_of(t_begin + 1, e1);
+        ahead(t_begin + 1);
     }
-    __syncthreads();
-    // column g of product b: this lane's dims [t D/4, (t+1) D/4) of its query
-    uint32_t qf[KI][NB][2];
-    float rf[NS][2];                        // score factor of queries 2t, 2t+1: 2^e scale log2(e)
-    int vis[NS][2];                         // keys they see
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (MODE == SPLIT && b == 1) break;
-        const int r = 8 * b + g;
-        const float* sq = &s_q[r][t * (D / 4)];
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < KI; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
-            amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+
+    // queries: D/4 lanes to each, four dims a lane; the first QB of a lane's QR on their way first
+    constexpr int QR = QT * (D / 4) / kWeigh > 0 ? QT * (D / 4) / kWeigh : 1, QB = QR < 4 ? QR : 4;
+    static_assert(QR * kWeigh >= QT * (D / 4), "all queries");
+    const int qd = (tid % (D / 4)) * 4;
+    auto q_of = [&](int j) { return j * (kWeigh / (D / 4)) + tid / (D / 4); };
+    auto fetch_q = [&](int r, Q4<TQ>& v) {      // false: nothing to see
+        if (r >= live) return false;
+        const int rr = r0 + r, i = rr / share, pos = L - n + i + rope.origin;
+        if (L - n + i < 0) return false;
+        if (rope.rot && (pos < 0 || pos >= rope.positions)) {
+            if (qd == 0) say(c.cap_code);
+            return false;
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        v.load(q, (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
+                      (size_t)(kvh * share + rr - i * share) * D, qd, rope, pos);
+        return true;
+    };
+    // ---------------------------------------------------------------- queries: fp16 columns
+    auto put_q = [&](int r, bool in, Q4<TQ>& v) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in) x = v.turned(qd, rope);
+        float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+        for (int o = D / 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (r >= QT) return;                    // (D = 64, N = 16: half of the threads have none)
         // bring the query near 1 by a power of two (exact); 2^+-100 keeps both factors finite
         int e2 = (int)(__float_as_uint(amax) >> 23) - 127;
         e2 = max(-100, min(100, e2));
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-        const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
+        x.x *= down, x.y *= down, x.z *= down, x.w *= down;
+        const uint32_t h0 = pack_h2(x.x, x.y), h1 = pack_h2(x.z, x.w);
 #pragma unroll
-        for (int k = 0; k < KI; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(sq + 4 * k);
-            const float x0 = x.x * down, x1 = x.y * down, x2 = x.z * down, x3 = x.w * down;
-            const uint32_t h0 = pack_h2(x0, x1), h1 = pack_h2(x2, x3);
-            qf[k][b][0] = h0;
-            qf[k][b][1] = h1;
-            if (MODE == SPLIT) {
-                qf[k][NB - 1][0] = rest_h2(x0, x1, h0);
-                qf[k][NB - 1][1] = rest_h2(x2, x3, h1);
-            }
+        for (int z = 0; z < PARTS; ++z) {
+            const int col = r * PARTS + z, ch = (qd & 63) >> 3;
+            *reinterpret_cast<uint2*>(Q16 + (qd >> 6) * (N * 128) + col * 128 +
+                                      ((ch ^ (col & 7)) << 4) + (qd & 4) * 2) =
+                z ? make_uint2(rest_h2(x.x, x.y, h0), rest_h2(x.z, x.w, h1)) : make_uint2(h0, h1);
         }
+        if (qd == 0) {
+            const int i = (r0 + r) / share, pos = L - n + i + rope.origin;
+            int vis = r < live ? max(0, L - n + i + 1) : 0;
+            if (rope.rot && (pos < 0 || pos >= rope.positions)) vis = 0;
+            s_rf[r] = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
+            s_m[r] = 0.f;
+            s_lag[r] = kNone;
+            s_vis[r] = vis;
+            s_out[r] = (int64_t)row * out.row + (int64_t)i * out.token +
+                       (int64_t)(kvh * share + (r0 + r - i * share)) * D;
+        }
+    };
+    if (warp < kWarps) {
+        Q4<TQ> q4[QB];
+        bool in[QB];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int col = 2 * t + e;
-            rf[b][e] = __shfl_sync(0xffffffffu, up, 4 * col);
-            const int rr = r0 + 8 * b + col, i = rr / share, pos = L - n + i + rope.origin;
-            vis[b][e] = rr < nq ? max(0, L - n + i + 1) : 0;
-            if (rope.rot && (pos < 0 || pos >= rope.positions)) vis[b][e] = 0;
+        for (int j0 = 0; j0 < QR; j0 += QB) {
+#pragma unroll
+            for (int j = 0; j < QB; ++j) in[j] = fetch_q(q_of(j0 + j), q4[j]);
+#pragma unroll
+            for (int j = 0; j < QB; ++j) put_q(q_of(j0 + j), in[j], q4[j]);
         }
+        fence_async_shared();
     }
+    __syncthreads();
     // a query without a rotation sees nothing: its column has to be masked from the first key on
-    bool lost = false;
-#pragma unroll
-    for (int b = 0; b < NS; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int col = 2 * t + e;
-            lost |= 8 * b + col < live && vis[b][e] < vis_min;
-        }
-    const int mask_from = __any_sync(0xffffffffu, lost) ? 0 : vis_min;
+    int lost = 0;
+    if (tid < live) lost = s_vis[tid] < vis_min;
+    const int mask_from = __syncthreads_or(lost) ? 0 : vis_min;
 
     // ---------------------------------------------------------------- the run
-    float m[NS][2], l[NS][2], O[VJ][NB][4];
+    const int T = t_end - t_begin;
+    const int half = (warp >> 2) & 1, key = tid & 127;      // a weighing thread's columns, and key
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t S = tmem + lanes + half * NC, O = tmem + lanes + 2 * N + half * NC;
+    float l[NQ];
 #pragma unroll
-    for (int b = 0; b < NS; ++b) m[b][0] = m[b][1] = -INFINITY, l[b][0] = l[b][1] = 0.f;
+    for (int i = 0; i < NQ; ++i) l[i] = 0.f;
+    if (converts) {
+        auto convert = [&](uint8_t* to, const uint4 (&b)[NL]) {
 #pragma unroll
-    for (int j = 0; j < VJ; ++j)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) O[j][b][0] = O[j][b][1] = O[j][b][2] = O[j][b][3] = 0.f;
-    const int key_lo = 4 * (g & 1) + (g >> 1);      // sigma(g): the key of row g; row g + 8: + 8
-
-    for (int it = 0; s_begin + it < s_end; ++it) {
-        cp_wait<NST - 2>();
-        __syncwarp();                       // the tile is here; every lane has left the last one
-        issue(it + NST - 1);
-        const uint8_t* st = ring + (it % NST) * SB;
-        const float4 meta = *reinterpret_cast<const float4*>(st + 2 * kTile * D);
-        const int k0 = (s_begin + it) * kTile;
-
-        float cf[NB][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) cf[b][0] = cf[b][1] = cf[b][2] = cf[b][3] = 0.f;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            uint4 x, y;
-            load_keys<D>(st, g, t, h, x, y);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t a[4];
-                h2x2_of(xs[k], a[0], a[2]);
-                h2x2_of(ys[k], a[1], a[3]);
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    mma_f16(cf[b], a, qf[4 * h + k][b][0], qf[4 * h + k][b][1]);
+            for (int j = 0; j < NL; ++j) {
+                const int r = cw * 16 + lr + 8 * (D == 128 ? j >> 1 : j);
+                uint8_t* at = to + (D == 128 ? (j & 1) * kAtom : 0) + r * 128;
+                uint4 x, y;
+                h2x2_of(b[j].x, x.x, x.y);
+                h2x2_of(b[j].y, x.z, x.w);
+                h2x2_of(b[j].z, y.x, y.y);
+                h2x2_of(b[j].w, y.z, y.w);
+                *reinterpret_cast<uint4*>(at + (((2 * lc) ^ (r & 7)) << 4)) = x;
+                *reinterpret_cast<uint4*>(at + (((2 * lc + 1) ^ (r & 7)) << 4)) = y;
             }
-        }
-        uint32_t vv[4][D / 32];
-        load_values<D>(st, g, t, vv);
-        // scores [key rows g, g + 8][queries 2t, 2t + 1], the value scale folded in
-        float s[NS][4];
-        if (MODE == SPLIT) {
+        };
+        for (int i = 0; i < T; ++i) {
+            const int b = i & 1, tile = t_begin + i;
+            if (i >= 2 && !wait(&s_s[b], i - 2)) break;     // tile i - 2's K is done with
+            convert(K16 + b * KV, kb);
+            uint32_t poison = 0;
+            if ((tile + 1) * kKeys > mask_from && mask_from < keys) {
+                // A value seen by some queries only: a NaN in it would reach the others as 0 x NaN,
+                // so it enters the product as 0 and the weights of those that see it become NaN.
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s[0][i] = fmaf(fmaf(cf[NB - 1][i], 1.f / 2048.f, cf[0][i]), rf[0][i & 1] * meta.x,
-                               meta.y);
-        } else {
+                for (int j = 0; j < NL; ++j) {
+                    uint32_t* w = &vb[j].x;
 #pragma unroll
-            for (int b = 0; b < NS; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[b][i] = fmaf(cf[b][i], rf[b][i & 1] * meta.x, meta.y);
-        }
-        const bool bad = !(meta.y > -INFINITY);
-        uint32_t poison = 0;                // keys of the tile with a NaN among their values
-        if (bad || k0 + kTile > mask_from) {    // the prefix ends in this tile for some query
-#pragma unroll
-            for (int b = 0; b < NS; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (bad || k0 + key_lo + 8 * (i >> 1) >= vis[b][i & 1]) s[b][i] = -INFINITY;
-            if (mask_from < vis_max) poison = clear_nan<D>(vv, t);
-        }
-        bool raise = false;
-        float mx[NS][2];
-#pragma unroll
-        for (int b = 0; b < NS; ++b)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mx[b][e] = fmaxf(s[b][e], s[b][2 + e]);
-                raise |= mx[b][e] > m[b][e] + kLag;
-            }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-            for (int b = 0; b < NS; ++b)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1)
-                        mx[b][e] = fmaxf(mx[b][e], __shfl_xor_sync(0xffffffffu, mx[b][e], o));
-                    const float mn = fmaxf(m[b][e], mx[b][e]);
-                    const float f = m[b][e] == mn ? 1.f : ex2(m[b][e] - mn);    // m = -inf: 0
-                    m[b][e] = mn;
-                    l[b][e] *= f;
-#pragma unroll
-                    for (int j = 0; j < VJ; ++j) {
-                        O[j][b][e] *= f, O[j][b][2 + e] *= f;
-                        if (MODE == SPLIT) O[j][NB - 1][e] *= f, O[j][NB - 1][2 + e] *= f;
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t z = ((w[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        if (z) poison |= 1u << (lr + 8 * (D == 128 ? j >> 1 : j));
+                        w[x] &= ~((z >> 7) * 0xffu);
                     }
                 }
-        }
-        uint32_t pb[NB][2];                 // the value product's operand
-#pragma unroll
-        for (int b = 0; b < NS; ++b) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float mm = m[b][i & 1];
-                p[i] = ex2(s[b][i] - (mm == -INFINITY ? 0.f : mm));
-                if (poison && s[b][i] != -INFINITY && ((poison >> (key_lo + 8 * (i >> 1))) & 1u))
-                    p[i] = NAN;
-                l[b][i & 1] = fmaf(p[i], meta.z, l[b][i & 1]);
+                poison = __reduce_or_sync(0xffffffffu, poison);
             }
+            if (lane == 0) {
+                s_meta[b][cw] = vs > 0.f ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f)
+                                         : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                s_poison[b][cw] = poison;
+            }
+            fence_async_shared();
+            arrive(&s_k[b]);
+            page_1 = page_2;
+            load_half(tile + 1, false, kb);
+            load_scales();
+            if (i >= 2 && !wait(&s_o[b], i - 2)) break;     // and its V
+            convert(V16 + b * KV, vb);
+            fence_async_shared();
+            arrive(&s_v[b]);
+            load_half(tile + 1, true, vb);
+            page_2 = page_of(tile + 2, entry);
+            ahead(tile + 2);
+            entry = entry_of(tile + 3);
+        }
+    } else if (warp == kWarps + kConvert) {
+        if (lane == 0) {
+            // descriptors count in 16 bytes: a step adds to them
+            const uint64_t k16 = tc::sdesc_k_sw128(tc::smem_u32(K16)),
+                           q16 = tc::sdesc_k_sw128(tc::smem_u32(Q16)),
+                           v16 = sdesc_mn_sw128(tc::smem_u32(V16)),
+                           w16 = sdesc_mn_sw128(tc::smem_u32(W16));
+            auto scores = [&](int i) {
+                const int b = i & 1;
+                if (!wait(&s_k[b], i)) return false;
+                tc::fence_after_sync();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float p0 = p[2 * h], p1 = p[2 * h + 1];
-                const uint32_t lead = pack_h2(p0, p1);
-                pb[b][h] = transpose8(lead);
-                if (MODE == SPLIT) pb[NB - 1][h] = transpose8(rest_h2(p0, p1, lead));
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16_ss(tmem + b * N,
+                               k16 + ((b * KV + (k >> 2) * kAtom + (k & 3) * 32) >> 4),
+                               q16 + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4),
+                               idesc_f16(N, false), k > 0);
+                tc::mma_commit(&s_s[b]);
+                return true;
+            };
+            bool ok = T > 0 && scores(0);
+            for (int i = 0; i < T && ok; ++i) {
+                // (tile i - 1's weights are there: S of tile i + 1 may overwrite its scores)
+                if (i + 1 < T) ok = scores(i + 1);
+                const int b = i & 1;
+                ok = ok && wait(&s_v[b], i) && wait(&s_w[b], i);
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_f16_ss(tmem + 2 * N, v16 + ((b * KV + k * 2048) >> 4),
+                               w16 + ((b * kAtom + k * 2048) >> 4), idesc_f16(N, true),
+                               i > 0 || k > 0);
+                tc::mma_commit(&s_o[b]);
             }
         }
+        __syncwarp();
+    } else {
+        auto vote = [&](bool x) {                           // any of the weighing threads
+            uint32_t any;
+            asm volatile(
+                "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n"
+                " barrier.cta.red.or.pred r, 1, %2, p;\n selp.u32 %0, 1, 0, r;\n}\n"
+                : "=r"(any)
+                : "r"((uint32_t)x), "n"(kWeigh)
+                : "memory");
+            __syncwarp();
+            return any != 0;
+        };
+        for (int i = 0; i < T; ++i) {
+            const int b = i & 1, k0 = (t_begin + i) * kKeys;
+            const bool tail = k0 + kKeys > mask_from;       // the prefix ends here for some query
+            bool ok = wait(&s_k[b], i) && wait(&s_s[b], i);         // the tile's scalars; its scores
+            ok = ok && (i < 2 || wait(&s_o[b], i - 2));             // and w's place is free
+            __syncwarp();
+            tc::fence_after_sync();
+            // scores of this thread's key, less the queries' maxima
+            const float4 meta = s_meta[b][key >> 4];
+            float x[NQ];
+            {
+                float cf[NC];
+                if constexpr (NC == 8) tmem_ld8(S + b * N, cf);
+                else if constexpr (NC == 16) tc::tmem_ld16(S + b * N, cf);
+                else tc::tmem_ld32(S + b * N, cf);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            // bytes of the four values paired (key 0, key 1) and (key 2, key 3): bytes 0, 1 and
-            // 2, 3 of word x are dims 4x .. 4x+3 of this lane
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t a[4];
-                h2x2_of(__byte_perm(vv[0][x], vv[1][x], y ? 0x7362 : 0x5140), a[0], a[1]);
-                h2x2_of(__byte_perm(vv[2][x], vv[3][x], y ? 0x7362 : 0x5140), a[2], a[3]);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) mma_f16(O[2 * x + y][b], a, pb[b][0], pb[b][1]);
+                for (int j = 0; j < NQ; ++j)
+                    x[j] = PARTS == 2 ? fmaf(cf[PARTS * j + PARTS - 1], 1.f / 2048.f, cf[PARTS * j])
+                                      : cf[j];
             }
+            bool raise = false;
+#pragma unroll
+            for (int j = 0; j < NQ; j += 4) {
+                const int at = (half * NQ + j) / 4;
+                const float4 rf = reinterpret_cast<const float4*>(s_rf)[at];
+                const float4 mq = reinterpret_cast<const float4*>(s_m)[at];
+                const float4 lag = reinterpret_cast<const float4*>(s_lag)[at];
+                x[j] = fmaf(x[j], rf.x * meta.x, meta.y) - mq.x;
+                x[j + 1] = fmaf(x[j + 1], rf.y * meta.x, meta.y) - mq.y;
+                x[j + 2] = fmaf(x[j + 2], rf.z * meta.x, meta.y) - mq.z;
+                x[j + 3] = fmaf(x[j + 3], rf.w * meta.x, meta.y) - mq.w;
+                if (tail) {
+                    const int4 vis = reinterpret_cast<const int4*>(s_vis)[at];
+                    if (k0 + key >= vis.x) x[j] = -INFINITY;
+                    if (k0 + key >= vis.y) x[j + 1] = -INFINITY;
+                    if (k0 + key >= vis.z) x[j + 2] = -INFINITY;
+                    if (k0 + key >= vis.w) x[j + 3] = -INFINITY;
+                }
+                raise |= x[j] > lag.x || x[j + 1] > lag.y || x[j + 2] > lag.z || x[j + 3] > lag.w;
+            }
+            if (meta.y == -INFINITY) {                      // no such key: not even a NaN of it
+                raise = false;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) x[j] = -INFINITY;
+            }
+            ok = ok && *(volatile int*)&s_abort == 0;
+            if (vote(raise || !ok)) {
+                if (vote(!ok)) break;                       // all of them
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const float y = x[j] == x[j] ? x[j] : -INFINITY;
+                    const float top = float_of(__reduce_max_sync(0xffffffffu, key_of(y)));
+                    if (lane == 0) s_red[warp & 3][half * NQ + j] = top;
+                }
+                vote(false);
+                if (tid < QT) {
+                    const float top = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]),
+                                            fmaxf(s_red[2][tid], s_red[3][tid]));
+                    const bool none = s_lag[tid] != kLag;   // sums of 0 so far
+                    const float up = none ? (top > kNone ? top : 0.f) : fmaxf(0.f, top);
+                    s_up[tid] = up;
+                    s_f[tid] = none ? 1.f : ex2(-up);
+                    s_m[tid] += up;
+                    if (top > kNone) s_lag[tid] = kLag;
+                }
+                if (i) ok = wait(&s_o[b ^ 1], i - 1);       // the product before this has finished
+                if (vote(!ok)) break;
+                tc::fence_after_sync();
+                float f[NC];
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const float r = s_f[half * NQ + j];
+                    x[j] -= s_up[half * NQ + j];
+                    l[j] *= r;
+#pragma unroll
+                    for (int z = 0; z < PARTS; ++z) f[PARTS * j + z] = r;
+                }
+                if (i)
+#pragma unroll
+                    for (int j = 0; j < NC; j += 8) {
+                        float o[8];
+                        tmem_ld8(O + j, o);
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) o[z] *= f[j + z];
+                        tmem_st8(O + j, o);
+                    }
+            }
+            const bool poisoned =
+                tail && mask_from < keys && ((s_poison[b][key >> 4] >> (key & 15)) & 1u);
+#pragma unroll
+            for (int j = 0; j < NC; j += 8) {               // weights, 8 columns at a time
+                uint32_t w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    float p[2];
+#pragma unroll
+                    for (int e = 0; e < (PARTS == 2 ? 1 : 2); ++e) {
+                        const int qi = PARTS == 2 ? j / 2 + z : j + 2 * z + e;
+                        p[e] = ex2(x[qi]);
+                        if (poisoned && x[qi] != -INFINITY) p[e] = NAN;
+                        l[qi] = fmaf(p[e], meta.z, l[qi]);
+                    }
+                    if (PARTS == 2) {
+                        const float h = __half2float(__float2half_rn(p[0]));
+                        w[z] = pack_h2(h, (p[0] - h) * 2048.f);
+                    } else {
+                        w[z] = pack_h2(p[0], p[PARTS == 2 ? 0 : 1]);
+                    }
+                }
+                const int ch = (half * NC + j) >> 3;
+                *reinterpret_cast<uint4*>(W16 + b * kAtom + key * 128 + ((ch ^ (key & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_async_shared();
+            tc::fence_before_sync();
+            arrive(&s_w[b]);
         }
+        if (T > 0) wait(&s_o[(T - 1) & 1], T - 1);
     }
-    cp_wait<0>();
-#pragma unroll
-    for (int b = 0; b < NS; ++b)            // the eight lanes of a column hold parts of its sum
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-                l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], o);
+    __syncthreads();
+    tc::fence_after_sync();
+    if (s_abort && tid == 0) say(c.late_code);              // a bounded wait gave up
 
     // ---------------------------------------------------------------- join
-    // shared memory: warps' O [4][QT][D], m and l [4][QT]; this CTA's O [QT][D], m, l [QT]
-    __syncthreads();
-    float* wO = reinterpret_cast<float*>(smem);
-    float* wM = wO + kWarps * QT * D;
-    float* wL = wM + kWarps * QT;
-    float* cO = wL + kWarps * QT;
-    float* cM = cO + QT * D;
-    float* cL = cM + QT;
-    static_assert((kWarps + 1) * (QT * D + 2 * QT) * 4 <= ring_bytes<D>(), "join fits the ring");
-    if (MODE == SPLIT) {                    // leading and trailing parts
+    // l over the 128 keys, then this CTA's O [query][D], m, l
+    float* const c_o = reinterpret_cast<float*>(K16);
+    float* const c_l = s_rf;                                // (the queries' factors are done with)
+    if (warp < kWarps) {
 #pragma unroll
-        for (int j = 0; j < VJ; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) O[j][0][i] = fmaf(O[j][NB - 1][i], 1.f / 2048.f, O[j][0][i]);
-    }
-#pragma unroll
-    for (int b = 0; b < NS; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 8 * b + 2 * t + e;
-            if (r < live) {
-                float* o = wO + (warp * QT + r) * D + g * (D / 8);
-#pragma unroll
-                for (int j = 0; j < VJ; ++j)
-                    *reinterpret_cast<float2*>(o + 2 * j) = make_float2(O[j][b][e], O[j][b][2 + e]);
-                if (g == 0) wM[warp * QT + r] = m[b][e], wL[warp * QT + r] = l[b][e];
-            }
+        for (int j = 0; j < NQ; ++j) {
+            const float s = warp_sum(l[j]);
+            if (lane == 0) s_red[warp & 3][half * NQ + j] = s;
         }
+    }
+    __syncthreads();
+    if (tid < QT) {
+        c_l[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+        if (s_lag[tid] != kLag) s_m[tid] = -INFINITY;       // a run without a score
+        s_f[tid] = c_l[tid] == 0.f ? 0.f : 1.f / c_l[tid];
+    }
     __syncthreads();
     auto put = [&](int r, int d, float o, float lsum) {
-        const int rr = r0 + r;
-        out.p[(int64_t)row * out.row + (int64_t)(rr / share) * out.token +
-              (int64_t)(kvh * share + rr % share) * D + d] =
-            from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
+        out.p[s_out[r] + d] = from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
     };
-    for (int x = threadIdx.x; x < live * D; x += kWarps * 32) {
-        const int r = x / D, d = x % D;
-        float M = wM[r];
+    if (warp < kWarps) {
+        const int dim = 32 * (warp & 3) + lane;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wM[w * QT + r]);
-        float o = 0.f, ls = 0.f;
+        for (int j = 0; j < NC; j += 8) {
+            float o[8];
+            if (T > 0) {
+                tmem_ld8(O + j, o);
+            } else {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = wM[w * QT + r];
-            const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-            o = fmaf(f, wO[(w * QT + r) * D + d], o);
-            ls = fmaf(f, wL[w * QT + r], ls);
-        }
-        if (nC == 1) {
-            put(r, d, o, ls);
-        } else {
-            cO[x] = o;
-            if (d == 0) cM[r] = M, cL[r] = ls;
+                for (int z = 0; z < 8; ++z) o[z] = 0.f;
+            }
+#pragma unroll
+            for (int z = 0; z < 8; z += PARTS) {
+                const int r = half * NQ + (j + z) / PARTS;
+                const float v = PARTS == 2 ? fmaf(o[z + PARTS - 1], 1.f / 2048.f, o[z]) : o[z];
+                if (r < live && dim < D) {
+                    if (nC == 1) out.p[s_out[r] + dim] = from_f<TO>(c_l[r] == 0.f ? 0.f : v * s_f[r]);
+                    else c_o[r * D + dim] = v;
+                }
+            }
         }
     }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, kCols);
     if (nC == 1) return;
     cluster.sync();                         // (CTAs without a run have exited)
-    for (int x = rank * kWarps * 32 + (int)threadIdx.x; x < live * D; x += nC * kWarps * 32) {
-        const int r = x / D, d = x % D;
-        float M = -INFINITY;
-        for (int k = 0; k < nC; ++k) M = fmaxf(M, *cluster.map_shared_rank(cM + r, k));
-        float o = 0.f, ls = 0.f;
-        for (int k = 0; k < nC; ++k) {
-            const float mk = *cluster.map_shared_rank(cM + r, k);
-            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-            o = fmaf(f, *cluster.map_shared_rank(cO + x, k), o);
-            ls = fmaf(f, *cluster.map_shared_rank(cL + r, k), ls);
-        }
-        put(r, d, o, ls);
-    }
+    join_cluster<D>(cluster, nC, rank, kThreads, live, c_o, s_m, c_l, reinterpret_cast<float*>(W16),
+                    put);
     cluster.sync();                         // no CTA leaves while its memory is read
 }
 
-template <int D, int MODE, int NB, typename TQ, typename TO>
+template <int D, int N, int PARTS, typename TQ, typename TO>
 cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int heads, int n,
                 const int32_t* lens, int lens_add, float scale, const Rope8& rope,
                 cudaStream_t st) {
-    constexpr int MT = queries_of(MODE, NB);
-    auto* kern = k_cache8_attend<D, MODE, NB, TQ, TO>;
+    auto* kern = k_cache8_attend<D, N, PARTS, TQ, TO>;
     const void* kp = reinterpret_cast<const void*>(kern);
-    const int share = heads / c.kv_heads, q_tiles = (n * share + MT - 1) / MT;
+    const int share = heads / c.kv_heads, q_tiles = (n * share + N / PARTS - 1) / (N / PARTS);
     int page_log2 = 4;
     while ((1 << page_log2) < c.page) ++page_log2;
     const int64_t cap = (int64_t)c.row_pages * c.page;
     const int C = ctas_of(cap);
     const int64_t ctas = (int64_t)c.rows * c.kv_heads * q_tiles * C;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (!set_smem_once(kp, ring_bytes<D>()) || (C > 8 && !set_wide_cluster_once(kp)))
+    constexpr size_t smem = smem_of<D, N>();
+    if (!set_smem_once(kp, smem) || (C > 8 && !set_wide_cluster_once(kp)))
         return cudaErrorInvalidConfiguration;
     set_carveout_once(kp);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = ring_bytes<D>();
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -483,16 +664,15 @@ cudaError_t launch_cache8_attend(const Cache8& c, Tok8<const TQ> q, int slabs, s
     if (c.rows <= 0 || n <= 0) return cudaSuccess;
     const QIn<TQ> qi{q.p, q.row, q.token, slabs, slab};
     const int64_t nq = (int64_t)n * (heads / c.kv_heads);
-#define RLT_RUN(MODE, NB)                                                                       \
-    (c.dh == 64 ? run<64, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)       \
-                : run<128, MODE, NB>(c, qi, out, heads, n, lens, lens_add, scale, rope, st))
     if (nq <= 4)
         return launch_cache8_decode<TQ, TO>(c, q, slabs, slab, out, heads, n, lens, lens_add, scale,
                                             rope, st);
-    if constexpr (std::is_same<TQ, bf16>::value && std::is_same<TO, bf16>::value)
-        return nq <= 8 ? RLT_RUN(PLAIN, 1) : RLT_RUN(PLAIN, 2);
-    else
-        return RLT_RUN(SPLIT, 2);
+    constexpr int P = std::is_same<TQ, bf16>::value && std::is_same<TO, bf16>::value ? 1 : 2;
+#define RLT_RUN(N)                                                                                \
+    (c.dh == 64 ? run<64, N, P>(c, qi, out, heads, n, lens, lens_add, scale, rope, st)            \
+                : run<128, N, P>(c, qi, out, heads, n, lens, lens_add, scale, rope, st))
+    const int64_t cols = nq * P;
+    return cols <= 16 ? RLT_RUN(16) : cols <= 32 ? RLT_RUN(32) : RLT_RUN(64);
 #undef RLT_RUN
 }
 

@@ -41,6 +41,7 @@ namespace cg = cooperative_groups;
 namespace rlt {
 namespace {
 
+constexpr int kQueries = 4;
 constexpr int kGroupRuns = 16;          // runs joined in one CTA
 constexpr int kMinTiles = 4;            // of a run
 constexpr int kMaxGroups = 16;          // CTAs of a cluster
@@ -64,9 +65,9 @@ __host__ __device__ __forceinline__ int run_tiles(int tiles, int groups) {
 
 // D = 64: 8 warps in 80 registers, three CTAs an SM; D = 128: two.  16 warps: one
 template <int D, int NW, typename TQ, typename TO>
-__global__ void __launch_bounds__(NW * 32, NW == 16 ? 1 : D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(NW * 32, NW == 16 ? 1 : 2)
 k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int units,
-                int unit_warps, int unit_runs, const int32_t* __restrict__ lens, int lens_add,
+                int unit_warps, int unit_slots, const int32_t* __restrict__ lens, int lens_add,
                 float scale_log2e, Rope8 rope) {
     constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -95,16 +96,38 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const int per = (run1 - run0 + unit_warps - 1) / unit_warps;
     const int r_begin = min(run1, run0 + wi * per), r_end = min(run1, r_begin + per);
     const int s_begin = r_begin * len, s_end = min(tiles, r_end * len);
-    // shared memory: the warps' tiles; per unit the queries (later the group's sums), its runs'
-    // O [run][query][D], m and l (padded to whole 16 bytes)
-    float* const s_unit = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
-                          here * (1 + unit_runs) * nq * (D + 4);
-    float* const s_o = s_unit + nq * (D + 4);
-    float* const s_m = s_o + unit_runs * nq * D;
-    float* const s_l = s_m + unit_runs * nq;
+    // Shared memory: the warps' tiles, then the sums of the runs, O [query][D], m and l, that a warp
+    // finishes before its last one.  The last one's go to the warp's own tiles, when they are done
+    // with; in the unit's first warp's tiles also the queries (a stage that is filled last) and
+    // the group's sums.
+    const int run_floats = nq * (D + 2);
+    uint8_t* const ring = smem + warp * (NST * SB);
+    uint8_t* const first = smem + here * unit_warps * (NST * SB);
+    float* const slots = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
+                         here * unit_slots * run_floats;
+    float* const s_q = reinterpret_cast<float*>(first + (NST - 1) * SB);    // [query][D + 4]
+    float* const g_o = reinterpret_cast<float*>(first + 4096);
+    float* const scratch = reinterpret_cast<float*>(first + 4096 + 2560);
+    static_assert(kQueries * (D + 4) * 4 <= SB && kQueries * (D + 2) * 4 <= 2560 &&
+                  4096 + 2560 + 3 * 16 * kQueries * 4 <= NST * SB, "they fit");
+
+    // ---------------------------------------------------------------- queries: on their way
+    const int qx = wi * 32 + lane;          // dims 4 qx .. of the unit's queries; the rest below
+    auto fetch_q = [&](int x, Q4<TQ>& v) {  // false: nothing to see
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        const int i = r / share, pos = L - n + i + rope.origin;
+        const bool seen = alive && L - n + i >= 0;
+        const bool lost = seen && rope.rot && (pos < 0 || pos >= rope.positions);
+        if (lost && d == 0 && c.status) atomicCAS(c.status, 0, c.cap_code);
+        if (!seen || lost) return false;
+        v.load(q, (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
+                      (size_t)(kvh * share + r % share) * D, d, rope, pos);
+        return true;
+    };
+    Q4<TQ> q4;
+    const bool q4_in = qx < nq * (D / 4) && fetch_q(qx, q4);
 
     // ---------------------------------------------------------------- tiles
-    uint8_t* ring = smem + warp * (NST * SB);
     const uint32_t ring_u = tc::smem_u32(ring);
     const size_t head_bytes = (size_t)D << page_log2;
     const size_t v_bytes = (size_t)c.kv_heads * head_bytes;
@@ -123,8 +146,8 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 b_page = p;
                 b_ks = __ldg(sc);
                 const float vs = __ldg(sc + c.kv_heads);
-                b_lv = log2f(vs);
-                b_inv = 1.f / vs;
+                b_lv = __log2f(vs);         // exact for powers of two, as rounded as fp32 for others
+                b_inv = __frcp_rn(vs);
             } else if (c.status) {
                 atomicCAS(c.status, 0, c.arg_code);
             }
@@ -161,19 +184,15 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 
     // ---------------------------------------------------------------- queries
     // rotated once per unit, then split into operands by every warp
-    for (int x = wi * 32 + lane; x < nq * (D / 4); x += unit_warps * 32) {
+    auto put_q = [&](int x, bool in, Q4<TQ>& v) {
         const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        const int i = r / share, pos = L - n + i + rope.origin;
-        const bool seen = alive && L - n + i >= 0;
-        const bool lost = seen && rope.rot && (pos < 0 || pos >= rope.positions);
-        if (lost && d == 0 && c.status) atomicCAS(c.status, 0, c.cap_code);
-        if (seen && !lost) {
-            const size_t at = (size_t)((int64_t)row * q.row + (int64_t)i * q.token) +
-                              (size_t)(kvh * share + r % share) * D;
-            load_q4(q, at, d, rope, pos, y);
-        }
-        *reinterpret_cast<float4*>(s_unit + r * (D + 4) + d) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(s_q + r * (D + 4) + d) =
+            in ? v.turned(d, rope) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (qx < nq * (D / 4)) put_q(qx, q4_in, q4);
+    for (int x = qx + unit_warps * 32; x < nq * (D / 4); x += unit_warps * 32) {
+        const bool in = fetch_q(x, q4);
+        put_q(x, in, q4);
     }
     __syncthreads();
     // column g: query g/2, this lane's dims [t D/4, (t+1) D/4) of it, leading or trailing bits
@@ -182,7 +201,7 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     int vis = 0;                            // keys it sees
     {
         const int r = g >> 1;
-        const float* sq = s_unit + r * (D + 4) + t * (D / 4);
+        const float* sq = s_q + r * (D + 4) + t * (D / 4);
         float amax = 0.f;
         if (r < nq)
 #pragma unroll
@@ -213,6 +232,7 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         vis = t < nq ? max(0, L - n + i + 1) : 0;
         if (rope.rot && (pos < 0 || pos >= rope.positions)) vis = 0;
     }
+    __syncthreads();                        // the stage that held the queries is filled from here on
     // a query without a rotation sees nothing: its column has to be masked from the first key on
     const int mask_from = __any_sync(0xffffffffu, t < nq && vis < vis_min) ? 0 : vis_min;
 
@@ -296,15 +316,20 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         if (--run_left == 0 || s + 1 == s_end) {        // the run's sums leave the registers
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            float* const to = run + 1 < r_end ? slots + (wi * (per - 1) + run - r_begin) * run_floats
+                                              : reinterpret_cast<float*>(ring);
+            if (s + 1 == s_end) {           // (the ring: no copy is on its way, none is read)
+                cp_wait<0>();
+                __syncwarp();
+            }
             if (t < nq) {
-                const int at = (run - run0) * nq + t;
-                float* o = s_o + at * D + g * (D / 8);
+                float* o = to + t * D + g * (D / 8);
 #pragma unroll
                 for (int j = 0; j < VJ; ++j)
                     *reinterpret_cast<float2*>(o + 2 * j) =
                         make_float2(fmaf(O[j][1], 1.f / 2048.f, O[j][0]),
                                     fmaf(O[j][3], 1.f / 2048.f, O[j][2]));
-                if (g == 0) s_m[at] = m, s_l[at] = l;
+                if (g == 0) to[nq * D + t] = m, to[nq * D + nq + t] = l;
             }
 #pragma unroll
             for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
@@ -322,50 +347,47 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
               (int64_t)(kvh * share + r % share) * D + d] =
             from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
     };
-    float* const g_m = s_unit + nq * D;             // the group's sums: O [query][D], m, l
-    float* const g_l = g_m + nq;
-    const int mine = run1 - run0;                   // (fewer than 0: none)
+    const int mine = run1 - run0;
+    // f(sums) for the runs in their order, warp by warp
+    auto each_run = [&](auto f) {
+        for (int w = 0, k = 0; k < mine; ++w) {
+            const float* z = slots + w * (per - 1) * run_floats;
+            const int last = min(mine, k + per) - 1;
+            for (; k < last; ++k, z += run_floats) f(z);
+            f(reinterpret_cast<const float*>(first + w * (NST * SB)));
+            ++k;
+        }
+    };
     if (alive)
         for (int x = wi * 32 + lane; x < nq * D; x += unit_warps * 32) {
             const int r = x / D, d = x % D;
             float M = -INFINITY;
-            for (int k = 0; k < mine; ++k) M = fmaxf(M, s_m[k * nq + r]);
+            each_run([&](const float* z) { M = fmaxf(M, z[nq * D + r]); });
             float o = 0.f, ls = 0.f;
-            for (int k = 0; k < mine; ++k) {
-                const float mk = s_m[k * nq + r];
+            each_run([&](const float* z) {
+                const float mk = z[nq * D + r];
                 const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-                o = fmaf(f, s_o[k * nq * D + x], o);
-                ls = fmaf(f, s_l[k * nq + r], ls);
-            }
+                o = fmaf(f, z[x], o);
+                ls = fmaf(f, z[nq * D + nq + r], ls);
+            });
             if (groups == 1) {
                 put(r, d, o, ls);
             } else {
-                s_unit[x] = o;
-                if (d == 0) g_m[r] = M, g_l[r] = ls;
+                g_o[x] = o;
+                if (d == 0) g_o[nq * D + r] = M, g_o[nq * D + nq + r] = ls;
             }
         }
     if (groups == 1) return;
     cluster.sync();                                 // (CTAs without a group have exited)
-    for (int x = rank * NW * 32 + (int)threadIdx.x; x < nq * D; x += groups * NW * 32) {
-        const int r = x / D, d = x % D;
-        float M = -INFINITY;
-        for (int k = 0; k < groups; ++k) M = fmaxf(M, *cluster.map_shared_rank(g_m + r, k));
-        float o = 0.f, ls = 0.f;
-        for (int k = 0; k < groups; ++k) {
-            const float mk = *cluster.map_shared_rank(g_m + r, k);
-            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-            o = fmaf(f, *cluster.map_shared_rank(s_unit + x, k), o);
-            ls = fmaf(f, *cluster.map_shared_rank(g_l + r, k), ls);
-        }
-        put(r, d, o, ls);
-    }
+    join_cluster<D>(cluster, groups, rank, NW * 32, nq, g_o, g_o + nq * D, g_o + nq * D + nq, scratch,
+                    put);
     cluster.sync();                                 // no CTA leaves while its memory is read
 }
 
 template <int D, int NW, typename TQ, typename TO>
 cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int share, int n,
                 const int32_t* lens, int lens_add, float scale, const Rope8& rope, int64_t units,
-                int C, int unit_warps, int unit_runs, size_t smem, cudaStream_t st) {
+                int C, int unit_warps, int unit_slots, size_t smem, cudaStream_t st) {
     auto* kern = k_cache8_decode<D, NW, TQ, TO>;
     const void* kp = reinterpret_cast<const void*>(kern);
     int page_log2 = 4;
@@ -391,7 +413,7 @@ cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int shar
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     const float scale_log2e = (float)((double)scale * 1.4426950408889634);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, c, page_log2, q, out, share, n, (int)units,
-                                       unit_warps, unit_runs, lens, lens_add, scale_log2e, rope);
+                                       unit_warps, unit_slots, lens, lens_add, scale_log2e, rope);
     if (e == cudaSuccess) rlt_count_launch();
     return e;
 }
@@ -405,24 +427,25 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
     const int C = groups_of(cap), nq = n * share;
     // runs that a group of a prefix up to the capacity can have: 16, or one per 64 keys
     const int unit_runs = (int)std::min<int64_t>(kGroupRuns, (cap / kTile + kMinTiles - 1) / kMinTiles);
-    auto smem = [&](int nw, int w) {
-        const int ring = nw == 16 ? ring_bytes<D, 16>() : ring_bytes<D, 8>();
-        return (size_t)ring + (size_t)(nw / w) * (1 + unit_runs) * nq * (D + 4) * 4;
+    // sums that a unit's w warps keep besides their last run's
+    auto slots = [&](int w) { return w * ((unit_runs + w - 1) / w - 1); };
+    auto smem = [&](int w) {
+        return (size_t)ring_bytes<D, 8>() + (size_t)(8 / w) * slots(w) * nq * (D + 2) * 4;
     };
-    // Warps of a unit: 16 where a few units are all there is and the sums fit beside their tiles;
-    // else as many as fill the machine (16 an SM), as long as the runs' sums leave room for as
-    // many CTAs.
-    const int64_t fill = 148 * 16;
-    if (unit_runs > 8 && units * C * 8 < fill && smem(16, 16) <= kMostSmem)
-        return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, 16, unit_runs,
-                          smem(16, 16), st);
+    // Warps of a unit.  16 where a few units are all there is (a cluster of 16 such CTAs, one an
+    // SM, finds a place in 7 of the GPU's 8 groups of SMs only: not there).  Else as few as fill
+    // the machine, 16 an SM (a warp starts and ends in about four tiles' time: 256 rows x 8 heads
+    // of at most 256 keys take 28 us with one warp, 20 with two), as long as the sums leave room
+    // for as many CTAs.
+    if (unit_runs > 8 && C <= 8 && units * C * 8 < 148 * 16)
+        return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, 16, 0,
+                          ring_bytes<D, 16>(), st);
     int w = 8;
-    if (C == 1)
-        while (w > 1 && (units * (w / 2) >= fill || w / 2 >= unit_runs) &&
-               smem(8, w / 2) <= (D == 64 ? 74 : 112) * 1024)
-            w /= 2;
-    return run<D, 8>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, w, unit_runs,
-                     smem(8, w), st);
+    while (C == 1 && w > 1 && (units * (w / 2) >= 148 * 16 || w / 2 >= unit_runs) &&
+           smem(w / 2) <= (D == 64 ? 74 : 113) * 1024)
+        w /= 2;
+    return run<D, 8>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, w, slots(w), smem(w),
+                     st);
 }
 
 }  // namespace

@@ -905,6 +905,7 @@ static rlt::Cache8 mem8_of(const rlt_state* s, int g, int b0, int rows) {
     return {(uint8_t*)s->mem + (size_t)g * n_pages * 2 * c.heads * kMem8Page * s->m->dh,
             s->mem8_scales + (size_t)g * n_pages * 2 * c.heads,
             s->mem8_table + (size_t)b0 * s->mem8_pages, s->err, rlt::kDevBounds, rlt::kDevCapacity,
+            rlt::kDevTimeout,
             (int)n_pages, rows, s->mem8_pages, kMem8Page, c.heads, s->m->dh};
 }
 // positions are 1-based: token j of a row is position j + 1

@@ -93,7 +93,7 @@ int check_rope(const rlt_rope* r, int dh, int dev) {
 }
 
 rlt::Cache8 cache_of(const rlt_cache8* c) {
-    return {(uint8_t*)c->pages, c->scales, c->table, c->status, RLT_E_ARG, RLT_E_CAPACITY,
+    return {(uint8_t*)c->pages, c->scales, c->table, c->status, RLT_E_ARG, RLT_E_CAPACITY, RLT_E_TIMEOUT,
             c->n_pages, c->rows, c->row_pages, c->page, c->kv_heads, c->dh};
 }
 rlt::Rope8 rope_of(const rlt_rope* r) {
