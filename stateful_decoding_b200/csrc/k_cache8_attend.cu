@@ -122,17 +122,20 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     constexpr int QT = N / PARTS;               // query vectors of a tile
     constexpr int NC = N / 2, NQ = QT / 2;      // a thread's columns, and queries
     constexpr int NL = D / 32;                  // a thread's 16-byte loads of K (and of V) per tile
-    constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (3 N used)
+    constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (of two tiles)
     extern __shared__ uint8_t raw[];
     // per query: score factor; maximum (0 before the first score); how far a score may pass it
     // (kNone before the first score); the last rise of the maximum, and what it leaves of the sums
     __shared__ __align__(16) float s_rf[QT], s_m[QT], s_lag[QT], s_up[QT], s_f[QT];
     __shared__ __align__(16) int s_vis[QT];
     __shared__ int64_t s_out[QT];               // where its output goes
-    __shared__ float4 s_meta[2][kKeys / 16];        // per 16 keys: ks, log2 vs, 1 / vs
-    __shared__ uint32_t s_poison[2][kKeys / 16];    // per 16 keys: those with a NaN value
+    // Of a tile's 16-key groups: ks, log2 vs, 1 / vs; the keys with a NaN value.  Four tiles': K of
+    // tile i + 2 is converted while tile i may still be weighed (V of i + 2 is not).
+    __shared__ float4 s_meta[4][kKeys / 16];
+    __shared__ uint32_t s_poison[4][kKeys / 16];
     __shared__ float s_red[4][QT];
     __shared__ __align__(8) uint64_t s_k[2], s_v[2], s_s[2], s_w[2], s_o[2];   // K, V, S, w there; O done
+    __shared__ __align__(8) uint64_t s_there[4];                              // a tile's s_meta
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -147,6 +150,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             tc::mbar_init(&s_w[b], kWarps);
             tc::mbar_init(&s_o[b], 1);
         }
+        for (int b = 0; b < 4; ++b) tc::mbar_init(&s_there[b], kConvert);
         s_abort = 0;
         tc::fence_mbar_init();
     }
@@ -187,14 +191,15 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     uint8_t* const W16 = V16 + 2 * KV;                      // 2 x weights [key][64 columns]
     uint8_t* const Q16 = W16 + 2 * kAtom;                   // [D/64][column][64 dims]
     // a bounded wait; once one gave up all do
-    auto wait = [&](uint64_t* bar, int i) {                 // for the barrier's use by tile i
+    auto wait_for = [&](uint64_t* bar, int use) {
         for (uint32_t polls = 0; polls < (1u << 22); ++polls) {
-            if (tc::mbar_try(bar, (uint32_t)(i >> 1) & 1u)) return true;
+            if (tc::mbar_try(bar, (uint32_t)use & 1u)) return true;
             if (*(volatile int*)&s_abort) return false;
         }
         *(volatile int*)&s_abort = 1;
         return false;
     };
+    auto wait = [&](uint64_t* bar, int i) { return wait_for(bar, i >> 1); };    // its use by tile i
     auto arrive = [&](uint64_t* bar) {                      // the warp's writes are done
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
@@ -336,9 +341,24 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const int half = (warp >> 2) & 1, key = tid & 127;      // a weighing thread's columns, and key
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + lanes + half * NC, O = tmem + lanes + 2 * N + half * NC;
-    float l[NQ];
+    float l[NQ], acc[PARTS == 2 ? NQ : 1];                  // (acc: PARTS = 2, below)
 #pragma unroll
     for (int i = 0; i < NQ; ++i) l[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < (PARTS == 2 ? NQ : 1); ++i) acc[i] = 0.f;
+    // PARTS = 2: a tile's O, leading and trailing parts, joins the others in fp32 registers (a
+    // thread's dim and its queries): the tensor cores' own sum over a long prefix truncates
+    auto add_tile = [&](int i) {
+        if constexpr (PARTS == 2) {
+#pragma unroll
+            for (int j = 0; j < NC; j += 8) {
+                float o[8];
+                tmem_ld8(O + (i & 1) * N + j, o);
+#pragma unroll
+                for (int z = 0; z < 8; z += 2) acc[(j + z) / 2] += fmaf(o[z + 1], 1.f / 2048.f, o[z]);
+            }
+        }
+    };
     if (converts) {
         auto convert = [&](uint8_t* to, const uint4 (&b)[NL]) {
 #pragma unroll
@@ -375,12 +395,13 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 poison = __reduce_or_sync(0xffffffffu, poison);
             }
             if (lane == 0) {
-                s_meta[b][cw] = vs > 0.f ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f)
+                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f)
                                          : make_float4(0.f, -INFINITY, 0.f, 0.f);
-                s_poison[b][cw] = poison;
+                s_poison[i & 3][cw] = poison;
             }
             fence_async_shared();
             arrive(&s_k[b]);
+            if (lane == 0) tc::mbar_arrive(&s_there[i & 3]);
             page_1 = page_2;
             load_half(tile + 1, false, kb);
             load_scales();
@@ -423,9 +444,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 tc::fence_after_sync();
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    mma_f16_ss(tmem + 2 * N, v16 + ((b * KV + k * 2048) >> 4),
+                    mma_f16_ss(tmem + 2 * N + (PARTS == 2 ? b * N : 0), v16 + ((b * KV + k * 2048) >> 4),
                                w16 + ((b * kAtom + k * 2048) >> 4), idesc_f16(N, true),
-                               i > 0 || k > 0);
+                               k > 0 || (PARTS == 1 && i > 0));
                 tc::mma_commit(&s_o[b]);
             }
         }
@@ -445,12 +466,12 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         for (int i = 0; i < T; ++i) {
             const int b = i & 1, k0 = (t_begin + i) * kKeys;
             const bool tail = k0 + kKeys > mask_from;       // the prefix ends here for some query
-            bool ok = wait(&s_k[b], i) && wait(&s_s[b], i);         // the tile's scalars; its scores
+            bool ok = wait_for(&s_there[i & 3], i >> 2) && wait(&s_s[b], i);     // scalars; scores
             ok = ok && (i < 2 || wait(&s_o[b], i - 2));             // and w's place is free
             __syncwarp();
             tc::fence_after_sync();
             // scores of this thread's key, less the queries' maxima
-            const float4 meta = s_meta[b][key >> 4];
+            const float4 meta = s_meta[i & 3][key >> 4];
             float x[NQ];
             {
                 float cf[NC];
@@ -487,6 +508,12 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) x[j] = -INFINITY;
             }
+            if (PARTS == 2 && i) {
+                ok = ok && wait(&s_o[b ^ 1], i - 1);
+                __syncwarp();
+                tc::fence_after_sync();
+                add_tile(i - 1);
+            }
             ok = ok && *(volatile int*)&s_abort == 0;
             if (vote(raise || !ok)) {
                 if (vote(!ok)) break;                       // all of them
@@ -510,27 +537,26 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 if (i) ok = wait(&s_o[b ^ 1], i - 1);       // the product before this has finished
                 if (vote(!ok)) break;
                 tc::fence_after_sync();
-                float f[NC];
+                // (the sums so far shrink: in registers, or in tensor memory)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
                     const float r = s_f[half * NQ + j];
                     x[j] -= s_up[half * NQ + j];
                     l[j] *= r;
-#pragma unroll
-                    for (int z = 0; z < PARTS; ++z) f[PARTS * j + z] = r;
+                    if (PARTS == 2) acc[PARTS == 2 ? j : 0] *= r;
                 }
-                if (i)
+                if (PARTS == 1 && i)
 #pragma unroll
                     for (int j = 0; j < NC; j += 8) {
                         float o[8];
                         tmem_ld8(O + j, o);
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) o[z] *= f[j + z];
+                        for (int z = 0; z < 8; ++z) o[z] *= s_f[half * NQ + j + z];
                         tmem_st8(O + j, o);
                     }
             }
             const bool poisoned =
-                tail && mask_from < keys && ((s_poison[b][key >> 4] >> (key & 15)) & 1u);
+                tail && mask_from < keys && ((s_poison[i & 3][key >> 4] >> (key & 15)) & 1u);
 #pragma unroll
             for (int j = 0; j < NC; j += 8) {               // weights, 8 columns at a time
                 uint32_t w[4];
@@ -559,7 +585,12 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             tc::fence_before_sync();
             arrive(&s_w[b]);
         }
-        if (T > 0) wait(&s_o[(T - 1) & 1], T - 1);
+        if (T > 0) {
+            wait(&s_o[(T - 1) & 1], T - 1);
+            __syncwarp();
+            tc::fence_after_sync();
+            add_tile(T - 1);
+        }
     }
     __syncthreads();
     tc::fence_after_sync();
@@ -591,7 +622,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
         for (int j = 0; j < NC; j += 8) {
             float o[8];
-            if (T > 0) {
+            if (PARTS == 1 && T > 0) {
                 tmem_ld8(O + j, o);
             } else {
 #pragma unroll
@@ -600,7 +631,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
             for (int z = 0; z < 8; z += PARTS) {
                 const int r = half * NQ + (j + z) / PARTS;
-                const float v = PARTS == 2 ? fmaf(o[z + PARTS - 1], 1.f / 2048.f, o[z]) : o[z];
+                const float v = PARTS == 2 ? acc[PARTS == 2 ? (j + z) / 2 : 0] : o[z];
                 if (r < live && dim < D) {
                     if (nC == 1) out.p[s_out[r] + dim] = from_f<TO>(c_l[r] == 0.f ? 0.f : v * s_f[r]);
                     else c_o[r * D + dim] = v;

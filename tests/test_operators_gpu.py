@@ -348,6 +348,38 @@ def test_attend(sd, case):
                 assert not out[b, i].any()
 
 
+ATTEND_BLOCKS = [
+    # many queries to a key head over many tiles and CTAs: lens, n, heads, kv, dh, page, type, rot
+    ([1000, 130], 4, 16, 2, 64, 32, "fp32", 0),         # 32 queries of two parts
+    ([1000, 130], 4, 16, 2, 64, 32, "bf16", 64),
+    ([2500, 3], 8, 16, 2, 64, 16, "bf16", 0),           # 64 queries
+    ([5000, 1], 2, 8, 1, 128, 64, "fp32", 128),
+    ([4096, 2048, 2049], 3, 8, 2, 128, 128, "fp32", 0),
+    ([9000, 513, 128, 127, 129], 2, 32, 1, 128, 16, "bf16", 0),
+    ([33000, 70], 1, 8, 1, 64, 128, "fp32", 64),        # 16 CTAs
+    ([12001], 16, 4, 1, 64, 64, "fp32", 0),             # 64 queries of two parts: two tiles
+    ([3000, 17], 16, 16, 2, 128, 64, "bf16", 128),      # 128 queries: two tiles
+]
+
+
+@pytest.mark.parametrize("case", ATTEND_BLOCKS, ids=[str(i) for i in range(len(ATTEND_BLOCKS))])
+def test_attend_blocks(sd, case):
+    import torch
+    lens, n, heads, kv, dh, page, t, rot = case
+    rope = _rope(sd, rot, max(lens) + 4)
+    cache = _new_cache(sd, len(lens), max(lens), page, kv, dh, seed=len(lens) + heads)
+    q = 2 * torch.randn(len(lens), n, heads, dh, generator=_gen(9), device="cuda")
+    q = q.float() if t == "fp32" else q.bfloat16()
+    out, again = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache.attend(q, ln, out, rope=rope)
+    cache.attend(q, ln, again, rope=rope)
+    torch.cuda.synchronize()
+    assert int(cache.status) == 0
+    _check_attend(cache, q, out, lens, dh ** -0.5, rope, t == "bf16")
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("dh,t,n,share", [(64, "fp32", 1, 1), (128, "bf16", 1, 2), (64, "bf16", 4, 3)])
 def test_attend_rows_do_not_depend_on_batch_capacity_or_run(sd, dh, t, n, share):
     """The same row alone, in a batch, in a table of another capacity, and twice: the same bits."""
