@@ -363,18 +363,14 @@ def _dtype_name(x) -> str:
     return name
 
 
+def _index(x):
+    """The index of a CUDA tensor's device; None for what is none (the checks then say so)."""
+    return x.get_device() if getattr(x, "is_cuda", False) else None
+
+
 def _device_buf(x, what: str, dtypes, shape=None, device=None):
     """Address of a CUDA tensor after its type, shape (None: any extent) and
-    device (an index) are checked; strides are the caller's to check.  The
-    calls below are a few microseconds long, so what is right passes in one
-    comparison each."""
-    try:
-        at = x.get_device()
-        if at >= 0 and (at == device or device is None) and _dtype_name(x) in dtypes and \
-                (shape is None or x.shape == shape):
-            return x.data_ptr()
-    except AttributeError:
-        pass
+    device (an index) are checked; strides are the caller's to check."""
     if not getattr(x, "is_cuda", False):
         raise TypeError(f"{what}: expected a CUDA tensor, got {type(x).__name__}"
                         f"{' on the host' if hasattr(x, 'data_ptr') else ''}")
@@ -390,8 +386,16 @@ def _device_buf(x, what: str, dtypes, shape=None, device=None):
     return x.data_ptr()
 
 
-def _dense(x, what: str, *args, **kw):
-    p = _device_buf(x, what, *args, **kw)
+# The calls below take a few microseconds, most of them here: what is right passes in one
+# comparison each, and only what did not is looked at again to say what is wrong.
+def _dense(x, what: str, dtypes, shape=None, device=None):
+    try:
+        if 0 <= x.get_device() == device and _dtype_names[x.dtype] in dtypes and x.shape == shape and \
+                x.is_contiguous():
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    p = _device_buf(x, what, dtypes, shape, device)
     if not x.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
     return p
@@ -400,6 +404,13 @@ def _dense(x, what: str, *args, **kw):
 def _heads_tensor(x, what: str, dtypes, shape, device):
     """Address, row pitch and token pitch of a [rows][n][heads][dh] tensor whose heads are
     adjacent."""
+    try:
+        if 0 <= x.get_device() == device and _dtype_names[x.dtype] in dtypes and x.shape == shape:
+            row, token, head, one = x.stride()
+            if one == 1 and head == shape[3]:
+                return x.data_ptr(), row, token
+    except (AttributeError, KeyError):
+        pass
     p = _device_buf(x, what, dtypes, shape, device)
     row, token, head, one = x.stride()
     if x.numel() and (one != 1 or (head != shape[3] and shape[2] > 1)):
@@ -488,11 +499,14 @@ def beam_select(logits, scores, parents, tokens, new_scores, finished=None, new_
     """The k best continuations of each group's beams (rlt_beam_select): logits fp32 or bf16
     [groups][beams][vocab], scores fp32 [groups][beams], finished uint8 [groups][beams]; outputs
     parents and tokens int32, new_scores fp32, new_finished uint8, each [groups][k]."""
-    lp = _dense(logits, "logits", _DTYPES, (None, None, None))
-    groups, beams, vocab = logits.shape
-    dev = logits.get_device()
-    ps = parents.shape if len(getattr(parents, "shape", ())) == 2 else (groups, None)
-    k = ps[1]
+    shape = getattr(logits, "shape", ())
+    if len(shape) != 3 or len(getattr(parents, "shape", ())) != 2:
+        _dense(logits, "logits", _DTYPES, (None, None, None))
+        _dense(parents, "parents", ("int32",), (None, None))
+    groups, beams, vocab = shape
+    dev = _index(logits)
+    lp = _dense(logits, "logits", _DTYPES, shape, dev)
+    k = parents.shape[1]
     out, per = (groups, k), (groups, beams)
     pp = _dense(parents, "parents", ("int32",), out, dev)
     return _check(_lib.rlt_beam_select(
@@ -509,8 +523,10 @@ def rows_reorder(rows, parents, start: int = 0, stop: Optional[int] = None, stre
     [width] of any element type, the last two dimensions contiguous, parents int32
     [groups][beams]; positions [start, stop) of every plane of row g*beams + i take what row
     g*beams + parents[g][i] held."""
-    pp = _dense(parents, "parents", ("int32",), (None, None))
+    if len(getattr(parents, "shape", ())) != 2:
+        _dense(parents, "parents", ("int32",), (None, None))
     groups, beams = parents.shape
+    pp = _dense(parents, "parents", ("int32",), (groups, beams), _index(parents))
     if not getattr(rows, "is_cuda", False):
         raise TypeError("rows: expected a CUDA tensor")
     if rows.get_device() != parents.get_device():

@@ -40,7 +40,7 @@ namespace cg = cooperative_groups;
 namespace rlt {
 namespace {
 
-constexpr int NT = 512, NW = NT / 32;
+constexpr int NT = 256, NW = NT / 32;
 constexpr int NB = 4;                   // chunks per step of a thread
 constexpr int kCand = 1024;             // candidates a unit may collect
 constexpr int kSliceMin = 4096;         // logits of a slice at least
@@ -190,7 +190,7 @@ struct Unit {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT, 4)
 k_beam_select(const T* __restrict__ logits, const float* __restrict__ scores,
               const uint8_t* __restrict__ finished, int eos, float temperature, int beams,
               int vocab, int slices, int k, int32_t* __restrict__ parents,

@@ -273,9 +273,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     static_assert(QR * kWeigh >= QT * (D / 4), "all queries");
     const int qd = (tid % (D / 4)) * 4;
     auto q_of = [&](int j) { return j * (kWeigh / (D / 4)) + tid / (D / 4); };
-    auto fetch_q = [&](int r, Q4<TQ>& v) {      // false: nothing to see
+    auto fetch_q = [&](int r, int i, Q4<TQ>& v) {       // (of token i) false: nothing to see
         if (r >= live) return false;
-        const int rr = r0 + r, i = rr / share, pos = L - n + i + rope.origin;
+        const int rr = r0 + r, pos = L - n + i + rope.origin;
         if (L - n + i < 0) return false;
         if (rope.rot && (pos < 0 || pos >= rope.positions)) {
             if (qd == 0) say(c.cap_code);
@@ -286,7 +286,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         return true;
     };
     // ---------------------------------------------------------------- queries: fp16 columns
-    auto put_q = [&](int r, bool in, Q4<TQ>& v) {
+    auto put_q = [&](int r, int i, bool in, Q4<TQ>& v) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (in) x = v.turned(qd, rope);
         float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -307,7 +307,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 z ? make_uint2(rest_h2(x.x, x.y, h0), rest_h2(x.z, x.w, h1)) : make_uint2(h0, h1);
         }
         if (qd == 0) {
-            const int i = (r0 + r) / share, pos = L - n + i + rope.origin;
+            const int pos = L - n + i + rope.origin;
             int vis = r < live ? max(0, L - n + i + 1) : 0;
             if (rope.rot && (pos < 0 || pos >= rope.positions)) vis = 0;
             s_rf[r] = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
@@ -321,12 +321,16 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     if (warp < kWarps) {
         Q4<TQ> q4[QB];
         bool in[QB];
+        int of[QB];
 #pragma unroll
         for (int j0 = 0; j0 < QR; j0 += QB) {
 #pragma unroll
-            for (int j = 0; j < QB; ++j) in[j] = fetch_q(q_of(j0 + j), q4[j]);
+            for (int j = 0; j < QB; ++j) {
+                of[j] = (r0 + q_of(j0 + j)) / share;
+                in[j] = fetch_q(q_of(j0 + j), of[j], q4[j]);
+            }
 #pragma unroll
-            for (int j = 0; j < QB; ++j) put_q(q_of(j0 + j), in[j], q4[j]);
+            for (int j = 0; j < QB; ++j) put_q(q_of(j0 + j), of[j], in[j], q4[j]);
         }
         fence_async_shared();
     }
