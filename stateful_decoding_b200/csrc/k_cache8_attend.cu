@@ -28,7 +28,7 @@
 // The maximum of a query is raised only when a score passes it by 2^8 (one
 // barrier vote per tile); then the columns' maxima are found and O rescaled.
 //
-// Split.  The prefix of a (row, key head) is cut into runs of 2048 keys, or 8
+// Split.  The prefix of a (row, key head) is cut into runs of 2048 keys, or 4
 // longer ones (16 from 32768 keys on), for a CTA each, a function of that
 // prefix alone; they join through the cluster's distributed shared memory in
 // run order: no scratch, no atomics, and the same bits for a row whatever batch
@@ -50,7 +50,10 @@ constexpr int kKeys = 128;              // of a tile
 constexpr int kKeysPerCta = 2048;
 constexpr int64_t kLongKeys = 32768;    // from here on
 constexpr int kMaxCtas = 16;            // CTAs (one cluster) share a prefix, below
-constexpr int kFewCtas = 8;             // (clusters of 16 leave a quarter of the SMs idle)
+// Larger clusters wait for as many SMs of one group of SMs to be free at once: 16 rows of 20011 keys
+// x 4 key heads take 135, 149, 165, 214 us with at most 2, 4, 6, 8.  Fewer CTAs serve a few rows
+// worse: a row's own time grows (103 to 20011 keys: 133, 121, 118, 127 us).
+constexpr int kFewCtas = 4;
 constexpr float kNone = -3e38f;         // below every finite score
 constexpr uint32_t kAtom = kKeys * 128; // 64 dims of 128 keys in fp16
 
