@@ -358,7 +358,8 @@ int rlt_debug_set_positions(rlt_state* state, int row, int32_t pos_enc, int32_t 
  * attend: its keys are not seen); RLT_E_CAPACITY, a length below 0 or above
  * row_pages * page, or a position without a row in the rotation table (append:
  * those tokens are not written; attend: a length is cut to the capacity, a
- * query without a rotation gives 0).  The caller zeroes it.
+ * query without a rotation gives 0); RLT_E_TIMEOUT, a bounded wait inside
+ * attend gave up (its output is then undefined).  The caller zeroes it.
  * Table entries of blocks past a row's length are not read.  Pages may be
  * shared between rows for reading; a page that two rows of one append write
  * is undefined.
@@ -421,7 +422,8 @@ int rlt_cache8_append(const rlt_cache8* cache, int dtype, const void* k, int64_t
  * pitches in elements, heads adjacent, 16-byte multiples as above; out must not
  * overlap q.  lens: device int32 [rows].  Scores, the softmax and the sums are
  * fp32; with more than 4 query vectors per key head (n * heads / kv_heads) and
- * bf16 types, the probabilities enter the value product as fp16.  A row's
+ * bf16 types, a rotated query enters the score product and the probabilities
+ * the value product with 11 significant bits (fp16), else with 22.  A row's
  * result does not depend on the other rows, on `rows` or on row_pages, bit for
  * bit.  NaN in a value makes at least that dimension of the queries that see
  * it NaN, and of no others. */

@@ -37,6 +37,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// log2 of a positive normal value, exact for powers of two (the scales that appending chooses)
+__device__ __forceinline__ float log2_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u & 0x7fffffu ? __log2f(v) : (float)((int)(u >> 23) - 127);
+}
 // four e4m3 bytes as two pairs of fp16 values, exactly (NaN stays NaN)
 __device__ __forceinline__ void h2x2_of(uint32_t four, uint32_t& lo, uint32_t& hi) {
     asm("{\n"

@@ -28,6 +28,12 @@
 // The maximum of a query is raised only when a score passes it by 2^8 (one
 // barrier vote per tile); then the columns' maxima are found and O rescaled.
 //
+// 16 rows of 103 to 20011 keys x 4 key heads x 32 queries (165 MB) take 111-121 us against
+// 26 of the bytes: a tile takes about 2300 cycles (its conversion, its two products and
+// its weighing are some 1400 each and wait for one another), a CTA's start and end
+// about 17000.  (Sixteen queries a warp through m16n8k16 products, every key converted
+// by each warp: 174 us; one stage, two CTAs an SM: 121.)
+//
 // Split.  The prefix of a (row, key head) is cut into runs of 2048 keys, or 4
 // longer ones (16 from 32768 keys on), for a CTA each, a function of that
 // prefix alone; they join through the cluster's distributed shared memory in
@@ -402,7 +408,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 poison = __reduce_or_sync(0xffffffffu, poison);
             }
             if (lane == 0) {
-                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f)
+                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, log2_of(vs), __frcp_rn(vs), 0.f)
                                          : make_float4(0.f, -INFINITY, 0.f, 0.f);
                 s_poison[i & 3][cw] = poison;
             }

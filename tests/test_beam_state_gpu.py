@@ -119,6 +119,13 @@ def test_transitions_over_the_8_bit_memory(sd, kw, T):
     assert np.array_equal(got, again)
 
 
+def test_bytes_of_an_8_bit_memory(sd):
+    model, _ = _model(sd, BASE.replace(dtype=ri.DT_BF16))
+    plain, eight = sd.State(model, 2, 256), sd.State(model, 2, 256, mem8=True)
+    values = BASE.groups * 2 * BASE.heads * 256 * 64
+    assert plain.bytes()[0] - eight.bytes()[0] == 2 * values - (values + BASE.groups * 2 * BASE.heads * 4 * 4)
+
+
 def test_rows_restart_and_stand_at_unequal_positions(sd):
     """Packed documents over the 8-bit memory: each row as its last document alone."""
     model, _ = _model(sd, BASE)

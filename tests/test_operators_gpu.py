@@ -380,7 +380,38 @@ def test_attend_blocks(sd, case):
     assert torch.equal(out, again)
 
 
-@pytest.mark.parametrize("dh,t,n,share", [(64, "fp32", 1, 1), (128, "bf16", 1, 2), (64, "bf16", 4, 3)])
+@pytest.mark.parametrize("t", ["fp32", "bf16"])
+def test_attend_blocks_captured_and_on_two_streams(sd, t):
+    """Many queries to a key head: captured once and replayed with new lengths and queries, and
+    two calls at once."""
+    import torch
+    cache = _new_cache(sd, 3, 3000, 32, 2, 64, seed=8)
+    q = torch.randn(3, 5, 6, 64, generator=_gen(4), device="cuda")
+    q = q if t == "fp32" else q.bfloat16()
+    out, other, want = (torch.zeros_like(q) for _ in range(3))
+    lens = torch.tensor([3000, 5, 1200], dtype=torch.int32, device="cuda")
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    cache.attend(q, lens, out, stream=one)
+    cache.attend(q, lens, other, stream=two)
+    torch.cuda.synchronize()
+    cache.attend(q, lens, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(other, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        cache.attend(q, lens, out, stream=torch.cuda.current_stream())
+    for seed, new in ((1, [7, 2999, 0]), (2, [2048, 2049, 64])):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        q.normal_(generator=_gen(seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_attend(cache, q, out, new, 64 ** -0.5, None, t == "bf16")
+    assert int(cache.status) == 0
+
+
+@pytest.mark.parametrize("dh,t,n,share", [(64, "fp32", 1, 1), (128, "bf16", 1, 2), (64, "bf16", 4, 3),
+                                                (128, "fp32", 3, 3), (64, "bf16", 9, 2)])
 def test_attend_rows_do_not_depend_on_batch_capacity_or_run(sd, dh, t, n, share):
     """The same row alone, in a batch, in a table of another capacity, and twice: the same bits."""
     import torch
