@@ -438,14 +438,13 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
     auto smem = [&](int w) {
         return (size_t)ring_bytes<D, 8>() + (size_t)(8 / w) * slots(w) * nq * (D + 2) * 4;
     };
-    // Warps of a unit.  16 where a few units are all there is; of clusters of 16 such CTAs, one an
-    // SM, 7 run at a time, of 8-warp ones, two an SM, 14 (131072 keys: 4 key heads take 53 us with
-    // 16 warps, 8 take 103, and 98 with 8 warps).  Else 8; for
-    // short prefixes as few as fill the machine, 16 an SM (a warp starts and ends in about four
+    // Warps of a unit's CTA.  16 where all CTAs then run at once, one an SM (of clusters of 16, 7 do;
+    // 131072 keys: 4 key heads take 53 us with 16 warps, 8 take 103, and 98 with 8 warps; 256 CTAs,
+    // 16 rows x 16 heads of 4.3k keys, 66 and 51 us).  Else 8, two CTAs an SM; for short prefixes as few as fill the machine, 16 an SM (a warp starts and ends in about four
     // tiles' time: 256 rows x 8 heads of at most 256 keys take 28 us with one warp, 20 with two;
     // 48 rows x 16 heads of 2k to 8k keys 234 with four, 202 with 8), as long as the sums leave
     // room for as many CTAs.
-    if (unit_runs > 8 && units * C * 8 < 148 * 16 && (C <= 8 || (units + 6) / 7 < 2 * ((units + 13) / 14)))
+    if (unit_runs > 8 && units * C <= (C <= 8 ? 148 : 7 * 16))
         return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, 16, 0,
                           ring_bytes<D, 16>(), st);
     int w = 8;
