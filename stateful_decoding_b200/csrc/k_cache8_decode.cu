@@ -21,20 +21,20 @@
 // The maximum is raised only when a score passes it by 2^8 (one warp vote per
 // tile instead of a reduction); fp16 holds weights up to 2^16.
 //
-// Split.  A prefix is cut into runs of whole tiles: up to 16 of them of at
-// least 64 keys, twice as many for every doubling from 8192 keys on (256 at
-// most).  Every run's sums are kept apart and joined in run order, 16 runs at
-// a time in shared memory and then these groups through the cluster's
-// distributed shared memory: no scratch, no atomics, and the same bits for a
-// row whatever batch or capacity it sits in.  Who works on the runs is free:
-// a group's runs belong to 1 to 16 warps, as many as fill the machine, and a
-// warp's copies run on from one of its runs into the next.
+// Split.  A prefix is cut into a power of two of runs, 64 to 256 keys each (256
+// runs at most), and their sums are joined as the leaves of a binary tree:
+// pairs, pairs of pairs, ..., whoever works on them.  So the bits of a row do
+// not depend on the batch or capacity it sits in, while its runs go to as few
+// warps as fill the machine (8 for long prefixes in batches) or as many as there
+// are (a cluster of up to 16 CTAs for a single row).  A warp joins its own runs
+// as they end, a CTA its warps' results in shared memory, the cluster its CTAs'
+// through distributed shared memory: no scratch, no atomics.
 //
 // Bound by HBM for long batches: 64 rows x 16 heads x 4.3k keys x 128 (1.14 GB) take
-// 206 us, 5.5 TB/s, 0.86 of the copy rate; 16 warps an SM, about 300 instructions a
-// 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64 take 20 us (floor 5.5): their
+// 197 us, 5.8 TB/s, 0.9 of the copy rate; 16 warps an SM, about 300 instructions a
+// 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64 take 19 us (floor 5.5): their
 // warps start and end, four dependent loads deep, for a few tiles each.  One row of
-// 131072 keys x 8 heads takes 98 us (floor 42): 16 CTAs a head are a cluster's limit,
+// 131072 keys x 8 heads takes 83 us (floor 42): 16 CTAs a head are a cluster's limit,
 // and they pack on half of the SMs.
 #include <cooperative_groups.h>
 
@@ -48,32 +48,50 @@ namespace rlt {
 namespace {
 
 constexpr int kQueries = 4;
-constexpr int kGroupRuns = 16;          // runs joined in one CTA
-constexpr int kMinTiles = 4;            // of a run
-constexpr int kMaxGroups = 16;          // CTAs of a cluster
+constexpr int kMaxRuns = 256;
+constexpr int kMaxCtas = 16;            // of a cluster
 constexpr size_t kMostSmem = 227 * 1024;
-constexpr int64_t kGroupKeys = 4096;    // keys per group, from two groups on
 
 template <int D> constexpr int stages() { return D == 64 ? 4 : 3; }
 template <int D> constexpr int stage_bytes() { return 2 * kTile * D + 16; }
 template <int D, int NW> constexpr int ring_bytes() { return NW * stages<D>() * stage_bytes<D>(); }
 
-__host__ __device__ __forceinline__ int groups_of(int64_t keys) {
-    int g = 1;
-    while (g < kMaxGroups && 2 * g * kGroupKeys <= keys) g *= 2;
-    return g;
+// runs of a prefix: a power of two, of 4 tiles at least, 8 from 64 tiles on, 16 from 512 on (a run's
+// end costs about half a tile)
+__host__ __device__ __forceinline__ int runs_of(int tiles) {
+    const int most = tiles < 64 ? tiles / 4 : tiles < 512 ? tiles / 8 : tiles / 16;
+    int r = 1;
+    while (r < kMaxRuns && 2 * r <= most) r *= 2;
+    return r;
 }
-// tiles of a run
-__host__ __device__ __forceinline__ int run_tiles(int tiles, int groups) {
-    const int len = (tiles + kGroupRuns * groups - 1) / (kGroupRuns * groups);
-    return len > kMinTiles ? len : kMinTiles;
+// The sums of two neighbours in the tree, the left one's in m, l, its factor and the right one's
+// out: o = fa * o_left + fb * o_right, everywhere rounded alike
+__device__ __forceinline__ void join2(float& m, float& l, float m2, float l2, float& fa, float& fb) {
+    const float M = fmaxf(m, m2);
+    fa = m == -INFINITY ? 0.f : ex2(m - M);
+    fb = m2 == -INFINITY ? 0.f : ex2(m2 - M);
+    l = fmaf(fa, l, fb * l2);
+    m = M;
+}
+// The tree over N values (powers of two of them there, from the left; the others m = -inf, o = l =
+// 0, which change nothing): o, l of the root
+template <int N>
+__device__ __forceinline__ void join_tree(float (&m)[N], float (&l)[N], float (&o)[N]) {
+#pragma unroll
+    for (int s = 1; s < N; s *= 2)
+#pragma unroll
+        for (int k = 0; k < N; k += 2 * s) {
+            float fa, fb;
+            join2(m[k], l[k], m[k + s], l[k + s], fa, fb);
+            o[k] = fmaf(fa, o[k], fb * o[k + s]);
+        }
 }
 
-// D = 64: 8 warps in 80 registers, three CTAs an SM; D = 128: two.  16 warps: one
+// 8 warps: two CTAs an SM; 16: one
 template <int D, int NW, typename TQ, typename TO>
 __global__ void __launch_bounds__(NW * 32, NW == 16 ? 1 : 2)
 k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int units,
-                int unit_warps, int unit_slots, const int32_t* __restrict__ lens, int lens_add,
+                int unit_warps, int levels, const int32_t* __restrict__ lens, int lens_add,
                 float scale_log2e, Rope8 rope) {
     constexpr int NST = stages<D>(), SB = stage_bytes<D>(), KI = D / 16, VJ = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -95,22 +113,23 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         atomicCAS(c.status, 0, c.cap_code);
     const int keys = alive ? L : 0;                 // the last query sees all, the first:
     const int vis_min = L - n + 1;
-    const int tiles = (keys + kTile - 1) / kTile, groups = groups_of(keys);
-    if (rank >= groups) return;                     // (one unit per CTA then)
-    const int len = run_tiles(tiles, groups), runs = (tiles + len - 1) / len;
-    const int run0 = rank * kGroupRuns, run1 = min(runs, run0 + kGroupRuns);    // of this CTA
-    const int per = (run1 - run0 + unit_warps - 1) / unit_warps;
-    const int r_begin = min(run1, run0 + wi * per), r_end = min(run1, r_begin + per);
-    const int s_begin = r_begin * len, s_end = min(tiles, r_end * len);
-    // Shared memory: the warps' tiles, then the sums of the runs, O [query][D], m and l, that a warp
-    // finishes before its last one.  The last one's go to the warp's own tiles, when they are done
+    const int tiles = (keys + kTile - 1) / kTile, runs = runs_of(tiles);
+    // `per` runs a warp, warps 0 .. busy - 1 of CTAs 0 .. ctas - 1: all powers of two
+    const int per = max(1, runs / (C * unit_warps)), busy = min(unit_warps, runs / per);
+    const int ctas = max(1, runs / (per * unit_warps));
+    if (rank >= ctas) return;                       // (one unit per CTA then)
+    auto start_of = [&](int r) { return (int)((int64_t)r * tiles / runs); };
+    const int r_begin = (rank * unit_warps + wi) * per, r_end = wi < busy ? r_begin + per : r_begin;
+    const int s_begin = wi < busy ? start_of(r_begin) : 0, s_end = wi < busy ? start_of(r_end) : 0;
+    // Shared memory: the warps' tiles, then what a warp keeps of its unfinished subtrees, one level
+    // each: O [query][D], m and l.  A warp's result goes to its own tiles, when they are done
     // with; in the unit's first warp's tiles also the queries (a stage that is filled last) and
-    // the group's sums.
+    // the CTA's result.
     const int run_floats = nq * (D + 2);
     uint8_t* const ring = smem + warp * (NST * SB);
     uint8_t* const first = smem + here * unit_warps * (NST * SB);
-    float* const slots = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
-                         here * unit_slots * run_floats;
+    float* const stack = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
+                         warp * levels * run_floats;
     float* const s_q = reinterpret_cast<float*>(first + (NST - 1) * SB);    // [query][D + 4]
     float* const g_o = reinterpret_cast<float*>(first + 4096);
     float* const scratch = reinterpret_cast<float*>(first + 4096 + 2560);
@@ -247,7 +266,7 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
     for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
     const int key_lo = 4 * (g & 1) + (g >> 1);      // sigma(g): the key of row g; row g + 8: + 8
-    int slot = 0, run = r_begin, run_left = len;
+    int slot = 0, run = 0, run_end = start_of(r_begin + 1);     // (run: of this warp's)
 
     for (int s = s_begin; s < s_end; ++s) {
         cp_wait<NST - 2>();
@@ -319,31 +338,50 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 mma_f16(O[2 * x + y], a, b0, b1);
             }
         }
-        if (--run_left == 0 || s + 1 == s_end) {        // the run's sums leave the registers
+        if (s + 1 == run_end) {             // the run's sums, and those of the subtrees it completes
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            float* const to = run + 1 < r_end ? slots + (wi * (per - 1) + run - r_begin) * run_floats
-                                              : reinterpret_cast<float*>(ring);
-            if (s + 1 == s_end) {           // (the ring: no copy is on its way, none is read)
-                cp_wait<0>();
-                __syncwarp();
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) {
+                O[j][0] = fmaf(O[j][1], 1.f / 2048.f, O[j][0]);
+                O[j][2] = fmaf(O[j][3], 1.f / 2048.f, O[j][2]);
             }
+            const int at = t * D + g * (D / 8);
+            int level = 0;
+            for (; (run >> level) & 1; ++level) {
+                const float* const z = stack + level * run_floats;
+                if (t < nq) {
+                    float m1 = z[nq * D + t], l1 = z[nq * D + nq + t], fa, fb;
+                    join2(m1, l1, m, l, fa, fb);
+                    m = m1, l = l1;
+#pragma unroll
+                    for (int j = 0; j < VJ; ++j) {
+                        const float2 o = *reinterpret_cast<const float2*>(z + at + 2 * j);
+                        O[j][0] = fmaf(fa, o.x, fb * O[j][0]);
+                        O[j][2] = fmaf(fa, o.y, fb * O[j][2]);
+                    }
+                }
+            }
+            const bool last = s + 1 == s_end;
+            if (last) cp_wait<0>();         // (the ring: no copy is on its way,
+            __syncwarp();                   //  none is read; and the stack has been read)
+            float* const to = last ? reinterpret_cast<float*>(ring) : stack + level * run_floats;
             if (t < nq) {
-                float* o = to + t * D + g * (D / 8);
 #pragma unroll
                 for (int j = 0; j < VJ; ++j)
-                    *reinterpret_cast<float2*>(o + 2 * j) =
-                        make_float2(fmaf(O[j][1], 1.f / 2048.f, O[j][0]),
-                                    fmaf(O[j][3], 1.f / 2048.f, O[j][2]));
+                    *reinterpret_cast<float2*>(to + at + 2 * j) = make_float2(O[j][0], O[j][2]);
                 if (g == 0) to[nq * D + t] = m, to[nq * D + nq + t] = l;
             }
 #pragma unroll
             for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
             m = -INFINITY, l = 0.f;
             ++run;
-            run_left = len;
+            run_end = start_of(r_begin + run + 1);
         }
     }
+    if (tiles == 0 && wi == 0)              // no key: an empty sum
+        for (int x = lane; x < run_floats; x += 32)
+            reinterpret_cast<float*>(ring)[x] = x >= nq * D && x < nq * D + nq ? -INFINITY : 0.f;
     cp_wait<0>();
     __syncthreads();
 
@@ -353,47 +391,53 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
               (int64_t)(kvh * share + r % share) * D + d] =
             from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
     };
-    const int mine = run1 - run0;
-    // f(sums) for the runs in their order, warp by warp
-    auto each_run = [&](auto f) {
-        for (int w = 0, k = 0; k < mine; ++w) {
-            const float* z = slots + w * (per - 1) * run_floats;
-            const int last = min(mine, k + per) - 1;
-            for (; k < last; ++k, z += run_floats) f(z);
-            f(reinterpret_cast<const float*>(first + w * (NST * SB)));
-            ++k;
-        }
-    };
     if (alive)
         for (int x = wi * 32 + lane; x < nq * D; x += unit_warps * 32) {
-            const int r = x / D, d = x % D;
-            float M = -INFINITY;
-            each_run([&](const float* z) { M = fmaxf(M, z[nq * D + r]); });
-            float o = 0.f, ls = 0.f;
-            each_run([&](const float* z) {
-                const float mk = z[nq * D + r];
-                const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-                o = fmaf(f, z[x], o);
-                ls = fmaf(f, z[nq * D + nq + r], ls);
-            });
-            if (groups == 1) {
-                put(r, d, o, ls);
+            const int r = x / D;
+            float mm[NW], ll[NW], o[NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float* const z = reinterpret_cast<const float*>(first + w * (NST * SB));
+                mm[w] = -INFINITY, ll[w] = o[w] = 0.f;
+                if (w < busy) mm[w] = z[nq * D + r], ll[w] = z[nq * D + nq + r], o[w] = z[x];
+            }
+            join_tree<NW>(mm, ll, o);
+            if (ctas == 1) {
+                put(r, x - r * D, o[0], ll[0]);
             } else {
-                g_o[x] = o;
-                if (d == 0) g_o[nq * D + r] = M, g_o[nq * D + nq + r] = ls;
+                g_o[x] = o[0];
+                if (x == r * D) g_o[nq * D + r] = mm[0], g_o[nq * D + nq + r] = ll[0];
             }
         }
-    if (groups == 1) return;
-    cluster.sync();                                 // (CTAs without a group have exited)
-    join_cluster<D>(cluster, groups, rank, NW * 32, nq, g_o, g_o + nq * D, g_o + nq * D + nq, scratch,
-                    put);
+    if (ctas == 1) return;
+    cluster.sync();                                 // (CTAs without a run have exited)
+    for (int x = threadIdx.x; x < ctas * nq; x += NW * 32) {
+        const int k = x / nq, r = x - k * nq;
+        scratch[x] = *cluster.map_shared_rank(g_o + nq * D + r, k);
+        scratch[kMaxCtas * nq + x] = *cluster.map_shared_rank(g_o + nq * D + nq + r, k);
+    }
+    __syncthreads();
+    for (int x = rank * NW * 32 + (int)threadIdx.x; x < nq * D; x += ctas * NW * 32) {
+        const int r = x / D;
+        float mm[kMaxCtas], ll[kMaxCtas], o[kMaxCtas];
+#pragma unroll
+        for (int k = 0; k < kMaxCtas; ++k) {        // (the remote loads are all in flight at once)
+            mm[k] = -INFINITY, ll[k] = o[k] = 0.f;
+            if (k < ctas) {
+                o[k] = *cluster.map_shared_rank(g_o + x, k);
+                mm[k] = scratch[k * nq + r], ll[k] = scratch[(kMaxCtas + k) * nq + r];
+            }
+        }
+        join_tree<kMaxCtas>(mm, ll, o);
+        put(r, x - r * D, o[0], ll[0]);
+    }
     cluster.sync();                                 // no CTA leaves while its memory is read
 }
 
 template <int D, int NW, typename TQ, typename TO>
 cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int share, int n,
                 const int32_t* lens, int lens_add, float scale, const Rope8& rope, int64_t units,
-                int C, int unit_warps, int unit_slots, size_t smem, cudaStream_t st) {
+                int C, int unit_warps, int levels, size_t smem, cudaStream_t st) {
     auto* kern = k_cache8_decode<D, NW, TQ, TO>;
     const void* kp = reinterpret_cast<const void*>(kern);
     int page_log2 = 4;
@@ -419,7 +463,7 @@ cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int shar
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     const float scale_log2e = (float)((double)scale * 1.4426950408889634);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, c, page_log2, q, out, share, n, (int)units,
-                                       unit_warps, unit_slots, lens, lens_add, scale_log2e, rope);
+                                       unit_warps, levels, lens, lens_add, scale_log2e, rope);
     if (e == cudaSuccess) rlt_count_launch();
     return e;
 }
@@ -430,29 +474,32 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
                  cudaStream_t st) {
     const int64_t cap = (int64_t)c.row_pages * c.page, units = (int64_t)c.rows * c.kv_heads;
     if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const int C = groups_of(cap), nq = n * share;
-    // runs that a group of a prefix up to the capacity can have: 16, or one per 64 keys
-    const int unit_runs = (int)std::min<int64_t>(kGroupRuns, (cap / kTile + kMinTiles - 1) / kMinTiles);
-    // sums that a unit's w warps keep besides their last run's
-    auto slots = [&](int w) { return w * ((unit_runs + w - 1) / w - 1); };
-    auto smem = [&](int w) {
-        return (size_t)ring_bytes<D, 8>() + (size_t)(8 / w) * slots(w) * nq * (D + 2) * 4;
+    const int nq = n * share, runs = runs_of((int)((cap + kTile - 1) / kTile));
+    auto levels = [&](int w) {                      // of the tree in one of w warps
+        int v = 0;
+        while ((w << v) < runs) ++v;
+        return v;
     };
-    // Warps of a unit's CTA.  16 where all CTAs then run at once, one an SM (of clusters of 16, 7 do;
-    // 131072 keys: 4 key heads take 53 us with 16 warps, 8 take 103, and 98 with 8 warps; 256 CTAs,
-    // 16 rows x 16 heads of 4.3k keys, 66 and 51 us).  Else 8, two CTAs an SM; for short prefixes as few as fill the machine, 16 an SM (a warp starts and ends in about four
-    // tiles' time: 256 rows x 8 heads of at most 256 keys take 28 us with one warp, 20 with two;
-    // 48 rows x 16 heads of 2k to 8k keys 234 with four, 202 with 8), as long as the sums leave
-    // room for as many CTAs.
-    if (unit_runs > 8 && units * C <= (C <= 8 ? 148 : 7 * 16))
-        return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, 16, 0,
+    auto smem = [&](int w) {
+        return (size_t)ring_bytes<D, 8>() + (size_t)8 * levels(w) * nq * (D + 2) * 4;
+    };
+    // Warps of a unit.  Short prefixes: as few as fill the machine, 16 an SM (a warp starts and ends
+    // in about four tiles' time: 256 rows x 8 heads of at most 256 keys take 28 us with one warp,
+    // 20 with two).  Longer ones: 8 (48 rows x 16 heads of 2k to 8k keys: 234 us with four, 202
+    // with 8), and more as long as all run at once (9 rows x 16 heads of 4.3k keys: 50 us with 32,
+    // in two turns, 37 with 16).  More also where the subtrees leave no room for two CTAs an SM.
+    int w = std::min(cap <= 1024 ? 1 : 8, runs);
+    while (w < runs && w < 8 * kMaxCtas &&
+           (units * w * (cap <= 1024 ? 1 : 2) <= 148 * 16 || smem(w) > 113 * 1024))
+        w *= 2;
+    // CTAs of 16 warps, one an SM, for the few longest rows: of clusters of 16 such CTAs 7 run at
+    // a time, of 8-warp ones, two an SM, 14 (131072 keys: 4 key heads take 53 us with 16 warps a
+    // CTA, 8 take 103, and 98 with 8 warps)
+    if (runs == 16 * kMaxCtas && units <= 7)
+        return run<D, 16>(c, q, out, share, n, lens, lens_add, scale, rope, units, kMaxCtas, 16, 0,
                           ring_bytes<D, 16>(), st);
-    int w = 8;
-    while (cap <= 1024 && w > 1 && (units * (w / 2) >= 148 * 16 || w / 2 >= unit_runs) &&
-           smem(w / 2) <= (D == 64 ? 74 : 113) * 1024)
-        w /= 2;
-    return run<D, 8>(c, q, out, share, n, lens, lens_add, scale, rope, units, C, w, slots(w), smem(w),
-                     st);
+    return run<D, 8>(c, q, out, share, n, lens, lens_add, scale, rope, units, std::max(1, w / 8),
+                     std::min(w, 8), levels(w), smem(w), st);
 }
 
 }  // namespace

@@ -435,6 +435,25 @@ def test_attend_rows_do_not_depend_on_batch_capacity_or_run(sd, dh, t, n, share)
             assert torch.equal(one[0], out[b]), (b, blocks)
 
 
+@pytest.mark.parametrize("dh,t,share,rows,long", [(128, "bf16", 1, 40, 9000), (64, "fp32", 2, 70, 5000),
+                                                  (128, "bf16", 4, 24, 20000), (128, "fp32", 8, 12, 5000)])
+def test_attend_long_rows_do_not_depend_on_the_batch(sd, dh, t, share, rows, long):
+    """A batch that fills the machine gives a row few warps, a row alone gets many: the same bits."""
+    import torch
+    dt = torch.float32 if t == "fp32" else torch.bfloat16
+    lens = [long - 321 * b % long if b % 3 else 17 * b for b in range(rows)]
+    cache = _new_cache(sd, rows, long, 64, 4, dh, seed=2)
+    q = torch.randn(rows, 1, 4 * share, dh, generator=_gen(5), device="cuda").to(dt)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    cache.attend(q, ln, out)
+    for b in (0, 1, 2, rows - 1):
+        alone = sd.Cache8(cache.pages, cache.scales, cache.table[b:b + 1].contiguous())
+        one = torch.empty_like(q[:1])
+        alone.attend(q[b:b + 1].contiguous(), ln[b:b + 1].contiguous(), one)
+        assert torch.equal(one[0], out[b]), (b, lens[b])
+
+
 def test_attend_ignores_what_lies_behind_the_prefix(sd):
     """NaN bytes in every slot, page and scale past the prefix, and wild table entries past it."""
     import torch
