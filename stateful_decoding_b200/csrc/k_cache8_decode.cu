@@ -483,14 +483,16 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
     auto smem = [&](int w) {
         return (size_t)ring_bytes<D, 8>() + (size_t)8 * levels(w) * nq * (D + 2) * 4;
     };
-    // Warps of a unit.  Short prefixes: as few as fill the machine, 16 an SM (a warp starts and ends
-    // in about four tiles' time: 256 rows x 8 heads of at most 256 keys take 28 us with one warp,
-    // 20 with two).  Longer ones: 8 (48 rows x 16 heads of 2k to 8k keys: 234 us with four, 202
+    // Warps of a unit.  Short prefixes: as few as come near filling the machine, 12 an SM up to 512
+    // keys, then 16 (a warp starts and ends in about four tiles' time: 256 rows x 8 heads x 64 of
+    // 256 keys take 21 us with one warp, 25 with two; 128 rows x 16 heads x 128 of 1024 keys 100
+    // and 96).  Longer ones: 8 (48 rows x 16 heads of 2k to 8k keys: 234 us with four, 202
     // with 8), and more as long as all run at once (9 rows x 16 heads of 4.3k keys: 50 us with 32,
     // in two turns, 37 with 16).  More also where the subtrees leave no room for two CTAs an SM.
     int w = std::min(cap <= 1024 ? 1 : 8, runs);
     while (w < runs && w < 8 * kMaxCtas &&
-           (units * w * (cap <= 1024 ? 1 : 2) <= 148 * 16 || smem(w) > 113 * 1024))
+           ((cap <= 1024 ? units * w < 148 * (cap <= 512 ? 12 : 16) : units * w * 2 <= 148 * 16) ||
+            smem(w) > 113 * 1024))
         w *= 2;
     // CTAs of 16 warps, one an SM, for the few longest rows: of clusters of 16 such CTAs 7 run at
     // a time, of 8-warp ones, two an SM, 14 (131072 keys: 4 key heads take 53 us with 16 warps a
