@@ -15,8 +15,8 @@
 //              [dims/64][key][64 dims] serves K, read along the dims, and V,
 //              read across them;
 //   1 issues   the products: tile i + 1's first one before tile i's second;
-//   8 weigh    a thread of the first (second) four has one key and the first
-//              (second) half of the columns: weights need no exchange between
+//   8 weigh    (16 for 64 columns) a thread has one key and, by its set of four
+//              warps, 8 or 16 of the columns: weights need no exchange between
 //              lanes, and any number of queries keeps all lanes busy.
 //
 // PARTS = 2 (fp32 types): columns 2i and 2i + 1 hold query i's (weight i's)
@@ -50,8 +50,11 @@ namespace cg = cooperative_groups;
 namespace rlt {
 namespace {
 
-constexpr int kWarps = 8, kConvert = 8;     // that weigh; that convert; one more issues
-constexpr int kWeigh = 32 * kWarps, kThreads = 32 * (kWarps + kConvert + 1);
+constexpr int kConvert = 8;             // warps that convert
+// warps that weigh, four to a set of columns; one more issues (16 for 64 columns: 16 rows of 103 to
+// 20011 keys x 4 key heads x 128 queries take 294 us, 318 with 8; for 32 columns 135 and 122)
+constexpr int weigh_warps(int N) { return N == 64 ? 16 : 8; }
+constexpr int threads_of(int N) { return 32 * (weigh_warps(N) + kConvert + 1); }
 constexpr int kKeys = 128;              // of a tile
 constexpr int kKeysPerCta = 2048;
 constexpr int64_t kLongKeys = 32768;    // from here on
@@ -125,11 +128,12 @@ constexpr size_t smem_of() {
 
 // N columns of PARTS a query
 template <int D, int N, int PARTS, typename TQ, typename TO>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(N), 1)
 k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int n, int q_tiles,
                 const int32_t* __restrict__ lens, int lens_add, float scale_log2e, Rope8 rope) {
     constexpr int QT = N / PARTS;               // query vectors of a tile
-    constexpr int NC = N / 2, NQ = QT / 2;      // a thread's columns, and queries
+    constexpr int kWarps = weigh_warps(N), kWeigh = 32 * kWarps, kThreads = threads_of(N);
+    constexpr int NC = 4 * N / kWarps, NQ = NC / PARTS;     // a weighing thread's columns, and queries
     constexpr int NL = D / 32;                  // a thread's 16-byte loads of K (and of V) per tile
     constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (of two tiles)
     extern __shared__ uint8_t raw[];
@@ -351,9 +355,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 
     // ---------------------------------------------------------------- the run
     const int T = t_end - t_begin;
-    const int half = (warp >> 2) & 1, key = tid & 127;      // a weighing thread's columns, and key
+    const int part = warp >> 2, key = tid & 127;            // a weighing thread's columns, and key
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t S = tmem + lanes + half * NC, O = tmem + lanes + 2 * N + half * NC;
+    const uint32_t S = tmem + lanes + part * NC, O = tmem + lanes + 2 * N + part * NC;
     float l[NQ], acc[PARTS == 2 ? NQ : 1];                  // (acc: PARTS = 2, below)
 #pragma unroll
     for (int i = 0; i < NQ; ++i) l[i] = 0.f;
@@ -499,7 +503,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < NQ; j += 4) {
-                const int at = (half * NQ + j) / 4;
+                const int at = (part * NQ + j) / 4;
                 const float4 rf = reinterpret_cast<const float4*>(s_rf)[at];
                 const float4 mq = reinterpret_cast<const float4*>(s_m)[at];
                 const float4 lag = reinterpret_cast<const float4*>(s_lag)[at];
@@ -534,7 +538,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 for (int j = 0; j < NQ; ++j) {
                     const float y = x[j] == x[j] ? x[j] : -INFINITY;
                     const float top = float_of(__reduce_max_sync(0xffffffffu, key_of(y)));
-                    if (lane == 0) s_red[warp & 3][half * NQ + j] = top;
+                    if (lane == 0) s_red[warp & 3][part * NQ + j] = top;
                 }
                 vote(false);
                 if (tid < QT) {
@@ -553,8 +557,8 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 // (the sums so far shrink: in registers, or in tensor memory)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const float r = s_f[half * NQ + j];
-                    x[j] -= s_up[half * NQ + j];
+                    const float r = s_f[part * NQ + j];
+                    x[j] -= s_up[part * NQ + j];
                     l[j] *= r;
                     if (PARTS == 2) acc[PARTS == 2 ? j : 0] *= r;
                 }
@@ -564,7 +568,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                         float o[8];
                         tmem_ld8(O + j, o);
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) o[z] *= s_f[half * NQ + j + z];
+                        for (int z = 0; z < 8; ++z) o[z] *= s_f[part * NQ + j + z];
                         tmem_st8(O + j, o);
                     }
             }
@@ -590,7 +594,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                         w[z] = pack_h2(p[0], p[PARTS == 2 ? 0 : 1]);
                     }
                 }
-                const int ch = (half * NC + j) >> 3;
+                const int ch = (part * NC + j) >> 3;
                 *reinterpret_cast<uint4*>(W16 + b * kAtom + key * 128 + ((ch ^ (key & 7)) << 4)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -617,7 +621,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const float s = warp_sum(l[j]);
-            if (lane == 0) s_red[warp & 3][half * NQ + j] = s;
+            if (lane == 0) s_red[warp & 3][part * NQ + j] = s;
         }
     }
     __syncthreads();
@@ -643,7 +647,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             }
 #pragma unroll
             for (int z = 0; z < 8; z += PARTS) {
-                const int r = half * NQ + (j + z) / PARTS;
+                const int r = part * NQ + (j + z) / PARTS;
                 const float v = PARTS == 2 ? acc[PARTS == 2 ? (j + z) / 2 : 0] : o[z];
                 if (r < live && dim < D) {
                     if (nC == 1) out.p[s_out[r] + dim] = from_f<TO>(c_l[r] == 0.f ? 0.f : v * s_f[r]);
@@ -681,7 +685,7 @@ cudaError_t run(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int head
     set_carveout_once(kp);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(N));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
