@@ -110,3 +110,12 @@ def test_owners_refuse_host_tensors_and_wrong_types(sd):
         sd.Rope(torch.zeros(4, 32), torch.zeros(4, 32))
     with pytest.raises(TypeError):
         sd.beam_select(torch.zeros(1, 2, 8), torch.zeros(1, 2), None, None, None)
+
+
+def test_state_calls_refuse_nulls(sd):
+    out = ctypes.c_void_p()
+    assert sd._lib.rlt_state_create_with(None, 1, 8, 0, ctypes.byref(out)) == sd.RLT_E_ARG
+    assert sd.rlt_state_create_with(None, 1, 8, sd.STATE_MEM8)[0] == sd.RLT_E_ARG
+    a = np.zeros(4, np.int32)
+    assert sd.rlt_state_reorder(None, a, 2) == sd.RLT_E_ARG
+    assert sd.rlt_beam_step(None, a, None, -1, 1.0, 2, 0, a, a) == sd.RLT_E_ARG
