@@ -421,9 +421,15 @@ int rlt_cache8_append(const rlt_cache8* cache, int dtype, const void* k, int64_t
  * rope is not NULL.  q, out: `dtype` [rows][n][heads][dh] with row and token
  * pitches in elements, heads adjacent, 16-byte multiples as above; out must not
  * overlap q.  lens: device int32 [rows].  Scores, the softmax and the sums are
- * fp32; with more than 4 query vectors per key head (n * heads / kv_heads) and
- * bf16 types, a rotated query enters the score product and the probabilities
- * the value product with 11 significant bits (fp16), else with 22.  A row's
+ * fp32, and the value scales of a prefix may lie any distance apart (blocks of
+ * zeros, 2^-110, among them).  With up to 4 query vectors per key head
+ * (n * heads / kv_heads) a rotated query enters the score product and the
+ * probabilities the value product with 22 significant bits (fewer below 2^-29
+ * of the largest among 16 neighbouring keys).  With more, they do with 22 (fp32
+ * types) or 11 (bf16 types), and a probability times its value scale below
+ * 2^-20 of the query's largest is off by up to 2^-42 (bf16 types: 2^-31) of
+ * that: beside values that much larger, in any dimension, a query's other
+ * values lose bits, and beside an appended infinity they are lost.  A row's
  * result does not depend on the other rows, on `rows` or on row_pages, bit for
  * bit.  NaN in a value makes at least that dimension of the queries that see
  * it NaN, and of no others. */

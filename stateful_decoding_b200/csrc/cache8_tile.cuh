@@ -1,7 +1,6 @@
 // Pieces that the kernels of attention over the paged 8-bit cache share.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -12,7 +11,6 @@ namespace rlt {
 namespace {
 
 constexpr int kTile = 16;               // keys per step of a warp
-constexpr float kLag = 8.f;             // how far (log2) a score may pass the maximum
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -37,10 +35,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log2 of a positive normal value, exact for powers of two (the scales that appending chooses)
-__device__ __forceinline__ float log2_of(float v) {
-    const uint32_t u = __float_as_uint(v);
-    return u & 0x7fffffu ? __log2f(v) : (float)((int)(u >> 23) - 127);
+// a positive scale as m * 2^e, m in [1, 2) (subnormal ones are 2^-64 times a normal one)
+__device__ __forceinline__ void split_scale(float v, float& m, float& e) {
+    const bool small = v < 0x1p-126f;
+    const uint32_t u = __float_as_uint(small ? v * 0x1p64f : v);
+    m = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+    e = (float)((int)((u >> 23) & 255u) - (small ? 191 : 127));
 }
 // four e4m3 bytes as two pairs of fp16 values, exactly (NaN stays NaN)
 __device__ __forceinline__ void h2x2_of(uint32_t four, uint32_t& lo, uint32_t& hi) {
@@ -217,50 +217,6 @@ __device__ __forceinline__ uint32_t clear_nan(uint32_t (&vv)[4][D / 32], int t) 
         if (hit) poison |= 1u << (4 * i + t);
     }
     return __reduce_or_sync(0xffffffffu, poison);
-}
-
-// The CTAs' sums in a cluster's shared memory (O [query][D], m and l at the same places in each)
-// as one, in CTA order: this CTA's share of the outputs goes to put(query, dim, o, l).  `scratch`
-// holds 3 x 16 floats a query.  Every remote load of a thread is in flight at once: one after
-// another, 16 CTAs took 12 us.
-template <int D, typename Put>
-__device__ __forceinline__ void join_cluster(const cooperative_groups::cluster_group& cluster,
-                                             int ctas, int rank, int threads, int queries,
-                                             float* o_at, float* m_at, float* l_at, float* scratch,
-                                             Put put) {
-    constexpr int MOST = 16;
-    float* const s_m = scratch;             // [cta][query]: m, later its factor
-    float* const s_l = scratch + MOST * queries;
-    float* const s_sum = s_l + MOST * queries;
-    for (int x = threadIdx.x; x < ctas * queries; x += threads) {
-        const int k = x / queries, r = x - k * queries;
-        s_m[x] = *cluster.map_shared_rank(m_at + r, k);
-        s_l[x] = *cluster.map_shared_rank(l_at + r, k);
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < queries; r += threads) {
-        float M = -INFINITY, ls = 0.f;
-        for (int k = 0; k < ctas; ++k) M = fmaxf(M, s_m[k * queries + r]);
-        for (int k = 0; k < ctas; ++k) {
-            const float mk = s_m[k * queries + r];
-            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-            s_m[k * queries + r] = f;
-            ls = fmaf(f, s_l[k * queries + r], ls);
-        }
-        s_sum[r] = ls;
-    }
-    __syncthreads();
-    for (int x = rank * threads + (int)threadIdx.x; x < queries * D; x += ctas * threads) {
-        const int r = x / D;
-        float v[MOST];
-#pragma unroll
-        for (int k = 0; k < MOST; ++k) v[k] = k < ctas ? *cluster.map_shared_rank(o_at + x, k) : 0.f;
-        float o = 0.f;
-#pragma unroll
-        for (int k = 0; k < MOST; ++k)
-            if (k < ctas) o = fmaf(s_m[k * queries + r], v[k], o);
-        put(r, x - r * D, o, s_sum[r]);
-    }
 }
 
 }  // namespace

@@ -1,8 +1,13 @@
 // Attention over the paged 8-bit cache for 5 and more query vectors per key
 // head: blocks of tokens, shared key heads (include/rlt.h: rlt_cache8_attend).
 //
-// Mathematics, as for fewer queries (k_cache8_decode.cu): the value scale goes
-// into the exponent, so bytes enter both products as they are.  Here a CTA
+// Mathematics, as for fewer queries (k_cache8_decode.cu): bytes enter both
+// products as they are, value scales join the weights, and the sum of the
+// weights has an exponent of its own.  With a query's a (the largest score, when
+// it last rose) and whole number d (the largest s + log2 vs then, less a):
+// p_j = 2^(s_j - a), l = sum p_j, w_j = p_j vs_j 2^(7 - d),
+// o = sum w_j x^v_j / l * 2^(d - 7).  One exponent for both would lose the
+// weights of a page of zeros, whose scale is 2^-110.  Here a CTA
 // takes 128 keys at a time through the fifth-generation tensor cores, keys as
 // the rows of the first product and value dims as those of the second:
 //   S [128 keys][N]  = K [128][D] . Q^T       (K and Q row by row)
@@ -23,12 +28,14 @@
 // leading 11 bits and the next 11 bits times 2^11, added in fp32.  PARTS = 1
 // (bf16 types): leading bits alone.  Each query is brought near 1 by a power
 // of two first: a bf16 query is exact then, a rotated one is rounded to fp16
-// (half a step 2^-12), as weights are: below the bf16 output's 2^-9.
+// (half a step 2^-11 at most), as weights are: below the bf16 output's 2^-8.
+// fp16 holds 2^-14 to 2^16, so a weight keeps its bits down to 2^-20 of the
+// query's largest; below, it is off by 2^-31 (two parts: 2^-42) of that.
 //
-// The maximum of a query is raised only when a score passes it by 2^8 (one
+// a and d are raised only when a score or a weight passes them by 2^8 (one
 // barrier vote per tile); then the columns' maxima are found and O rescaled.
 //
-// 16 rows of 103 to 20011 keys x 4 key heads x 32 queries (165 MB) take 111-121 us against
+// 16 rows of 103 to 20011 keys x 4 key heads x 32 queries (165 MB) take 111-115 us against
 // 26 of the bytes: a tile takes about 2300 cycles (its conversion, its two products and
 // its weighing are some 1400 each and wait for one another), a CTA's start and end
 // about 17000.  (Sixteen queries a warp through m16n8k16 products, every key converted
@@ -40,6 +47,7 @@
 // run order: no scratch, no atomics, and the same bits for a row whatever batch
 // or capacity it sits in.
 #include <cooperative_groups.h>
+#include <float.h>
 
 #include <algorithm>
 
@@ -63,6 +71,8 @@ constexpr int kMaxCtas = 16;            // CTAs (one cluster) share a prefix, be
 // x 4 key heads take 135, 149, 165, 214 us with at most 2, 4, 6, 8.  Fewer CTAs serve a few rows
 // worse: a row's own time grows (103 to 20011 keys: 133, 121, 118, 127 us).
 constexpr int kFewCtas = 4;
+constexpr float kLag = 8.f;             // how far (log2) a score may pass a, with its value scale a + d
+constexpr float kUp = 7.f;              // weights are up to 2^(kLag + kUp), within fp16's 2^16
 constexpr float kNone = -3e38f;         // below every finite score
 constexpr uint32_t kAtom = kKeys * 128; // 64 dims of 128 keys in fp16
 
@@ -137,16 +147,18 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     constexpr int NL = D / 32;                  // a thread's 16-byte loads of K (and of V) per tile
     constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (of two tiles)
     extern __shared__ uint8_t raw[];
-    // per query: score factor; maximum (0 before the first score); how far a score may pass it
-    // (kNone before the first score); the last rise of the maximum, and what it leaves of the sums
-    __shared__ __align__(16) float s_rf[QT], s_m[QT], s_lag[QT], s_up[QT], s_f[QT];
+    // per query: score factor; a (0 before the first score); how far a score and log2 of its value
+    // scale together may pass a (kLag + d; kNone before the first score); 2^(kUp - d); the last rise of
+    // a, and what it leaves of l and of O
+    __shared__ __align__(16) float s_rf[QT], s_m[QT], s_room[QT], s_g[QT], s_up[QT], s_f[QT], s_fo[QT];
     __shared__ __align__(16) int s_vis[QT];
     __shared__ int64_t s_out[QT];               // where its output goes
-    // Of a tile's 16-key groups: ks, log2 vs, 1 / vs; the keys with a NaN value.  Four tiles': K of
+    // Of a tile's 16-key groups: ks, vs, log2 vs or the whole number above (-inf: no such keys); the
+    // keys with a NaN value.  Four tiles': K of
     // tile i + 2 is converted while tile i may still be weighed (V of i + 2 is not).
     __shared__ float4 s_meta[4][kKeys / 16];
     __shared__ uint32_t s_poison[4][kKeys / 16];
-    __shared__ float s_red[4][QT];
+    __shared__ float s_red[4][QT], s_red2[4][QT];
     __shared__ __align__(8) uint64_t s_k[2], s_v[2], s_s[2], s_w[2], s_o[2];   // K, V, S, w there; O done
     __shared__ __align__(8) uint64_t s_there[4];                              // a tile's s_meta
     __shared__ int s_abort;
@@ -325,7 +337,8 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             if (rope.rot && (pos < 0 || pos >= rope.positions)) vis = 0;
             s_rf[r] = __uint_as_float((uint32_t)(127 + e2) << 23) * scale_log2e;
             s_m[r] = 0.f;
-            s_lag[r] = kNone;
+            s_room[r] = kNone;
+            s_g[r] = 1.f;
             s_vis[r] = vis;
             s_out[r] = (int64_t)row * out.row + (int64_t)i * out.token +
                        (int64_t)(kvh * share + (r0 + r - i * share)) * D;
@@ -412,8 +425,10 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 poison = __reduce_or_sync(0xffffffffu, poison);
             }
             if (lane == 0) {
-                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, log2_of(vs), __frcp_rn(vs), 0.f)
-                                         : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                float vm, ve;
+                split_scale(vs, vm, ve);
+                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, vs, vm > 1.f ? ve + 1.f : ve, 0.f)
+                                         : make_float4(0.f, 0.f, -INFINITY, 0.f);
                 s_poison[i & 3][cw] = poison;
             }
             fence_async_shared();
@@ -487,7 +502,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             ok = ok && (i < 2 || wait(&s_o[b], i - 2));             // and w's place is free
             __syncwarp();
             tc::fence_after_sync();
-            // scores of this thread's key, less the queries' maxima
+            // scores of this thread's key, less the queries' a
             const float4 meta = s_meta[i & 3][key >> 4];
             float x[NQ];
             {
@@ -506,11 +521,11 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 const int at = (part * NQ + j) / 4;
                 const float4 rf = reinterpret_cast<const float4*>(s_rf)[at];
                 const float4 mq = reinterpret_cast<const float4*>(s_m)[at];
-                const float4 lag = reinterpret_cast<const float4*>(s_lag)[at];
-                x[j] = fmaf(x[j], rf.x * meta.x, meta.y) - mq.x;
-                x[j + 1] = fmaf(x[j + 1], rf.y * meta.x, meta.y) - mq.y;
-                x[j + 2] = fmaf(x[j + 2], rf.z * meta.x, meta.y) - mq.z;
-                x[j + 3] = fmaf(x[j + 3], rf.w * meta.x, meta.y) - mq.w;
+                const float4 room = reinterpret_cast<const float4*>(s_room)[at];
+                x[j] = fmaf(x[j], rf.x * meta.x, -mq.x);
+                x[j + 1] = fmaf(x[j + 1], rf.y * meta.x, -mq.y);
+                x[j + 2] = fmaf(x[j + 2], rf.z * meta.x, -mq.z);
+                x[j + 3] = fmaf(x[j + 3], rf.w * meta.x, -mq.w);
                 if (tail) {
                     const int4 vis = reinterpret_cast<const int4*>(s_vis)[at];
                     if (k0 + key >= vis.x) x[j] = -INFINITY;
@@ -518,9 +533,12 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                     if (k0 + key >= vis.z) x[j + 2] = -INFINITY;
                     if (k0 + key >= vis.w) x[j + 3] = -INFINITY;
                 }
-                raise |= x[j] > lag.x || x[j + 1] > lag.y || x[j + 2] > lag.z || x[j + 3] > lag.w;
+                raise |= x[j] > fminf(kLag, room.x - meta.z) ||
+                         x[j + 1] > fminf(kLag, room.y - meta.z) ||
+                         x[j + 2] > fminf(kLag, room.z - meta.z) ||
+                         x[j + 3] > fminf(kLag, room.w - meta.z);
             }
-            if (meta.y == -INFINITY) {                      // no such key: not even a NaN of it
+            if (meta.z == -INFINITY) {                      // no such key: not even a NaN of it
                 raise = false;
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) x[j] = -INFINITY;
@@ -538,18 +556,33 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 for (int j = 0; j < NQ; ++j) {
                     const float y = x[j] == x[j] ? x[j] : -INFINITY;
                     const float top = float_of(__reduce_max_sync(0xffffffffu, key_of(y)));
-                    if (lane == 0) s_red[warp & 3][part * NQ + j] = top;
+                    const float top2 = float_of(__reduce_max_sync(0xffffffffu, key_of(y + meta.z)));
+                    if (lane == 0) s_red[warp & 3][part * NQ + j] = top, s_red2[warp & 3][part * NQ + j] = top2;
                 }
                 vote(false);
                 if (tid < QT) {
                     const float top = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]),
                                             fmaxf(s_red[2][tid], s_red[3][tid]));
-                    const bool none = s_lag[tid] != kLag;   // sums of 0 so far
-                    const float up = none ? (top > kNone ? top : 0.f) : fmaxf(0.f, top);
-                    s_up[tid] = up;
-                    s_f[tid] = none ? 1.f : ex2(-up);
-                    s_m[tid] += up;
-                    if (top > kNone) s_lag[tid] = kLag;
+                    const float top2 = fmaxf(fmaxf(s_red2[0][tid], s_red2[1][tid]),
+                                             fmaxf(s_red2[2][tid], s_red2[3][tid]));
+                    if (top > kNone) {                      // (else no score, here or so far: as it was)
+                        const bool none = s_room[tid] == kNone;     // sums of 0 so far
+                        // (the largest score itself: a key that dwarfs the others weighs exactly 1)
+                        const float up = none ? top : fmaxf(0.f, top);
+                        const float left = s_room[tid] - kLag - up;         // d, were it to stay a + d
+                        // -118: 2^(kUp - d) stays finite; nothing but scales below 2^-110 comes near
+                        float d = fmaxf(-118.f, ceilf(top2 - up));
+                        if (!none) d = fmaxf(d, ceilf(left));
+                        s_up[tid] = up;
+                        s_f[tid] = none ? 1.f : ex2(-up);
+                        s_fo[tid] = none ? 1.f : ex2(left - d);
+                        s_m[tid] += up;
+                        s_room[tid] = kLag + d;
+                        s_g[tid] = ex2(kUp - d);
+                    } else {
+                        s_up[tid] = 0.f;
+                        s_f[tid] = s_fo[tid] = 1.f;
+                    }
                 }
                 if (i) ok = wait(&s_o[b ^ 1], i - 1);       // the product before this has finished
                 if (vote(!ok)) break;
@@ -557,10 +590,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 // (the sums so far shrink: in registers, or in tensor memory)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const float r = s_f[part * NQ + j];
                     x[j] -= s_up[part * NQ + j];
-                    l[j] *= r;
-                    if (PARTS == 2) acc[PARTS == 2 ? j : 0] *= r;
+                    l[j] *= s_f[part * NQ + j];
+                    if (PARTS == 2) acc[PARTS == 2 ? j : 0] *= s_fo[part * NQ + j];
                 }
                 if (PARTS == 1 && i)
 #pragma unroll
@@ -568,7 +600,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                         float o[8];
                         tmem_ld8(O + j, o);
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) o[z] *= s_f[part * NQ + j + z];
+                        for (int z = 0; z < 8; ++z) o[z] *= s_fo[part * NQ + j + z];
                         tmem_st8(O + j, o);
                     }
             }
@@ -577,15 +609,25 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
             for (int j = 0; j < NC; j += 8) {               // weights, 8 columns at a time
                 uint32_t w[4];
+                float f[8 / PARTS];                         // (finite: a weight of 0 stays 0)
+#pragma unroll
+                for (int z = 0; z < 8 / PARTS; z += 4) {
+                    const float4 g = reinterpret_cast<const float4*>(s_g)[(part * NQ + j / PARTS + z) / 4];
+                    f[z] = fminf(meta.y * g.x, FLT_MAX);
+                    f[z + 1] = fminf(meta.y * g.y, FLT_MAX);
+                    f[z + 2] = fminf(meta.y * g.z, FLT_MAX);
+                    f[z + 3] = fminf(meta.y * g.w, FLT_MAX);
+                }
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     float p[2];
 #pragma unroll
                     for (int e = 0; e < (PARTS == 2 ? 1 : 2); ++e) {
-                        const int qi = PARTS == 2 ? j / 2 + z : j + 2 * z + e;
+                        const int at = PARTS == 2 ? z : 2 * z + e, qi = j / PARTS + at;
                         p[e] = ex2(x[qi]);
                         if (poisoned && x[qi] != -INFINITY) p[e] = NAN;
-                        l[qi] = fmaf(p[e], meta.z, l[qi]);
+                        l[qi] += p[e];
+                        p[e] *= f[at];
                     }
                     if (PARTS == 2) {
                         const float h = __half2float(__float2half_rn(p[0]));
@@ -625,15 +667,16 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         }
     }
     __syncthreads();
+    float* const c_d = s_room;
     if (tid < QT) {
         c_l[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
-        if (s_lag[tid] != kLag) s_m[tid] = -INFINITY;       // a run without a score
-        s_f[tid] = c_l[tid] == 0.f ? 0.f : 1.f / c_l[tid];
+        if (c_d[tid] == kNone) s_m[tid] = -INFINITY, c_d[tid] = 0.f;     // a run without a score
+        else c_d[tid] -= kLag;
+        const float by = c_d[tid] - kUp, half = floorf(0.5f * by);      // 2^by / l in two factors
+        s_f[tid] = c_l[tid] == 0.f ? 0.f : ex2(half) / c_l[tid];
+        s_fo[tid] = ex2(by - half);
     }
     __syncthreads();
-    auto put = [&](int r, int d, float o, float lsum) {
-        out.p[s_out[r] + d] = from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
-    };
     if (warp < kWarps) {
         const int dim = 32 * (warp & 3) + lane;
 #pragma unroll
@@ -650,7 +693,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 const int r = part * NQ + (j + z) / PARTS;
                 const float v = PARTS == 2 ? acc[PARTS == 2 ? (j + z) / 2 : 0] : o[z];
                 if (r < live && dim < D) {
-                    if (nC == 1) out.p[s_out[r] + dim] = from_f<TO>(c_l[r] == 0.f ? 0.f : v * s_f[r]);
+                    if (nC == 1)
+                        out.p[s_out[r] + dim] =
+                            from_f<TO>(c_l[r] == 0.f ? 0.f : v * s_f[r] * s_fo[r]);
                     else c_o[r * D + dim] = v;
                 }
             }
@@ -661,8 +706,52 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);
     if (nC == 1) return;
     cluster.sync();                         // (CTAs without a run have exited)
-    join_cluster<D>(cluster, nC, rank, kThreads, live, c_o, s_m, c_l, reinterpret_cast<float*>(W16),
-                    put);
+    // Every CTA's sums as one, in CTA order, each by its factor; this CTA's share of the outputs.
+    // Every remote load of a thread is in flight at once: one after another, 16 CTAs took 12 us.
+    float* const j_a = reinterpret_cast<float*>(W16);       // [cta][query]: a, later O's factor
+    float* const j_d = j_a + kMaxCtas * QT;
+    float* const j_l = j_d + kMaxCtas * QT;
+    float* const j_sum = j_l + kMaxCtas * QT;               // l of all, and 2^(a + d - kUp) in two
+    float* const j_by = j_sum + QT;
+    static_assert((3 * kMaxCtas + 2) * QT * 4 <= 2 * kAtom, "they fit");
+    for (int x = tid; x < nC * live; x += kThreads) {
+        const int k = x / live, r = x - k * live;
+        j_a[x] = *cluster.map_shared_rank(s_m + r, k);
+        j_d[x] = *cluster.map_shared_rank(c_d + r, k);
+        j_l[x] = *cluster.map_shared_rank(c_l + r, k);
+    }
+    __syncthreads();
+    for (int r = tid; r < live; r += kThreads) {
+        float top = -INFINITY, a = -INFINITY, d = 0.f, most = -INFINITY, ls = 0.f;
+        for (int k = 0; k < nC; ++k) {          // the largest a; a and d of the largest a + d
+            const float ak = j_a[k * live + r], dk = j_d[k * live + r];
+            top = fmaxf(top, ak);
+            if (ak + dk > most) most = ak + dk, a = ak, d = dk;
+        }
+        for (int k = 0; k < nC; ++k) {
+            const int x = k * live + r;
+            const float ak = j_a[x];
+            const bool none = ak == -INFINITY;
+            ls = fmaf(none ? 0.f : ex2(ak - top), j_l[x], ls);
+            j_a[x] = none ? 0.f : ex2((ak - a) + (j_d[x] - d));
+        }
+        j_sum[r] = ls;
+        j_by[r] = (a - top) + (d - kUp);
+    }
+    __syncthreads();
+    for (int x = rank * kThreads + tid; x < live * D; x += nC * kThreads) {
+        const int r = x / D;
+        float v[kMaxCtas];
+#pragma unroll
+        for (int k = 0; k < kMaxCtas; ++k) v[k] = k < nC ? *cluster.map_shared_rank(c_o + x, k) : 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCtas; ++k)
+            if (k < nC) o = fmaf(j_a[k * live + r], v[k], o);
+        const float by = j_by[r], half = floorf(0.5f * by);
+        out.p[s_out[r] + x - r * D] =
+            from_f<TO>(j_sum[r] == 0.f ? 0.f : o / j_sum[r] * ex2(half) * ex2(by - half));
+    }
     cluster.sync();                         // no CTA leaves while its memory is read
 }
 

@@ -3,11 +3,15 @@
 //
 // Mathematics.  With byte values x, key scales ks and value scales vs per
 // (page, head), o = sum_j p_j vs_j x^v_j / sum_j p_j, p_j = 2^(s_j),
-// s_j = scale log2(e) ks_j q.x^k_j.  The value scale is folded into the
-// exponent: w_j = 2^(s_j + log2 vs_j - m) with m a running maximum of
-// s + log2 vs, so that o = sum w_j x^v_j / sum (w_j / vs_j): bytes enter the
-// two products as they are (e4m3 is exact in fp16), a 16-key tile needs two
-// scalars per head, and w stays within fp16's range whatever the scales.
+// s_j = scale log2(e) ks_j q.x^k_j.  Bytes enter the two products as they are
+// (e4m3 is exact in fp16).  A tile of 16 keys lies in one page, so its weights
+// are brought to its own largest score, p_j = 2^(s_j - t) with t whole and
+// s_j <= t (2^15 p_j in fp16), and its product sum_j p_j x^v_j joins the others in
+// fp32 by the factor vs 2^(t - e), the sum of the p_j by 2^(t - a): e and a are
+// whole numbers that rise with the largest t + log2 vs and the largest t.  Two
+// exponents, so that value scales cost the weights nothing, however far apart: a
+// page of zeros has the scale 2^-110, one with an infinity 2^120.  A tile is lost
+// only where it is 2^-190 of the largest (in o) or 2^-126 (in l).
 //
 // Matrix form.  One warp takes 16 keys at a time through m16n8k16 fp16
 // products with fp32 sums, keys (then value dims) as the 16 rows, queries as
@@ -18,11 +22,9 @@
 // 11 bits times 2^11: a lane meets both sums of a score, and adds them in
 // fp32.  The weights pass from the score product's layout to the value
 // product's operand by an 8x8 transpose of the warp's registers (movmatrix).
-// The maximum is raised only when a score passes it by 2^8 (one warp vote per
-// tile instead of a reduction); fp16 holds weights up to 2^16.
 //
-// Split.  A prefix is cut into a power of two of runs, 64 to 256 keys each (256
-// runs at most), and their sums are joined as the leaves of a binary tree:
+// Split.  A prefix is cut into a power of two of runs, of 64 to 256 keys up to 65536 keys (256
+// runs at most, longer then), and their sums are joined as the leaves of a binary tree:
 // pairs, pairs of pairs, ..., whoever works on them.  So the bits of a row do
 // not depend on the batch or capacity it sits in, while its runs go to as few
 // warps as fill the machine (8 for long prefixes in batches) or as many as there
@@ -31,11 +33,12 @@
 // through distributed shared memory: no scratch, no atomics.
 //
 // Bound by HBM for long batches: 64 rows x 16 heads x 4.3k keys x 128 (1.14 GB) take
-// 197 us, 5.8 TB/s, 0.9 of the copy rate; 16 warps an SM, about 300 instructions a
-// 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64 take 19 us (floor 5.5): their
-// warps start and end, four dependent loads deep, for a few tiles each.  One row of
-// 131072 keys x 8 heads takes 83 us (floor 42): 16 CTAs a head are a cluster's limit,
-// and they pack on half of the SMs.
+// 204-219 us from one B200 to another, 5.2-5.6 TB/s, 0.8-0.87 of the copy rate; 16 warps an SM,
+// about 350 instructions a 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64 take
+// 21 us (floor 5.5): their warps start and end, four dependent loads deep, for a few tiles
+// each (1 us of it the tiles' largest scores, three shuffles each).  One row of 131072 keys x 8
+// heads takes 87 us (floor 42): 16 CTAs a head are a cluster's limit, and they pack on
+// half of the SMs.  (Products added in pairs by packed fp32 instructions: 220 and 91 us.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -64,25 +67,44 @@ __host__ __device__ __forceinline__ int runs_of(int tiles) {
     while (r < kMaxRuns && 2 * r <= most) r *= 2;
     return r;
 }
-// The sums of two neighbours in the tree, the left one's in m, l, its factor and the right one's
-// out: o = fa * o_left + fb * o_right, everywhere rounded alike
-__device__ __forceinline__ void join2(float& m, float& l, float m2, float l2, float& fa, float& fb) {
-    const float M = fmaxf(m, m2);
-    fa = m == -INFINITY ? 0.f : ex2(m - M);
-    fb = m2 == -INFINITY ? 0.f : ex2(m2 - M);
-    l = fmaf(fa, l, fb * l2);
-    m = M;
+constexpr float kNone = -3e38f;         // exponent of an empty sum
+constexpr float kAhead = 64.f;          // a new largest tile's factor, log2,
+constexpr float kMost = 72.f;           // and the factor from which on the exponent rises
+// A tile's product is at most 2^28 (16 keys, weights of 2^15, bytes of 448), with its factor 2^101;
+// 2^30 keys are 2^26 tiles: below fp32's 2^128.
+
+constexpr float kWeight = 15.f;         // log2 of the weights' factor in fp16
+
+// 2^x, subnormal results included
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-// The tree over N values (powers of two of them there, from the left; the others m = -inf, o = l =
-// 0, which change nothing): o, l of the root
+// Sums over some keys: l of weights, in units of 2^a; o of weighted values (one a dim), in units of 2^e
+struct Sum {
+    float a, e, l;
+};
+// The sums of two neighbours in the tree, the left one's in x, its factor and the right one's
+// out: o = fa * o_left + fb * o_right, everywhere rounded alike
+__device__ __forceinline__ void join2(Sum& x, const Sum& y, float& fa, float& fb) {
+    const float A = fmaxf(x.a, y.a), E = fmaxf(x.e, y.e);
+    x.l = fmaf(ex2(x.a - A), x.l, ex2(y.a - A) * y.l);
+    fa = pow2(x.e - E);
+    fb = pow2(y.e - E);
+    x.a = A;
+    x.e = E;
+}
+// The tree over N values, the first `there` of them (a power of two): the root's in x[0], o[0]
 template <int N>
-__device__ __forceinline__ void join_tree(float (&m)[N], float (&l)[N], float (&o)[N]) {
+__device__ __forceinline__ void join_tree(Sum (&x)[N], float (&o)[N], int there) {
 #pragma unroll
     for (int s = 1; s < N; s *= 2)
 #pragma unroll
         for (int k = 0; k < N; k += 2 * s) {
+            if (k + s >= there) break;
             float fa, fb;
-            join2(m[k], l[k], m[k + s], l[k + s], fa, fb);
+            join2(x[k], x[k + s], fa, fb);
             o[k] = fmaf(fa, o[k], fb * o[k + s]);
         }
 }
@@ -122,10 +144,10 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const int r_begin = (rank * unit_warps + wi) * per, r_end = wi < busy ? r_begin + per : r_begin;
     const int s_begin = wi < busy ? start_of(r_begin) : 0, s_end = wi < busy ? start_of(r_end) : 0;
     // Shared memory: the warps' tiles, then what a warp keeps of its unfinished subtrees, one level
-    // each: O [query][D], m and l.  A warp's result goes to its own tiles, when they are done
-    // with; in the unit's first warp's tiles also the queries (a stage that is filled last) and
-    // the CTA's result.
-    const int run_floats = nq * (D + 2);
+    // each: O [query][D], then the queries' a, e and l (a multiple of 4 floats in all).  A warp's
+    // result goes to its own tiles, when they are done with; in the unit's first warp's tiles also
+    // the queries (a stage that is filled last) and the CTA's result.
+    const int run_floats = nq * (D + 4);
     uint8_t* const ring = smem + warp * (NST * SB);
     uint8_t* const first = smem + here * unit_warps * (NST * SB);
     float* const stack = reinterpret_cast<float*>(smem + ring_bytes<D, NW>()) +
@@ -133,7 +155,7 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     float* const s_q = reinterpret_cast<float*>(first + (NST - 1) * SB);    // [query][D + 4]
     float* const g_o = reinterpret_cast<float*>(first + 4096);
     float* const scratch = reinterpret_cast<float*>(first + 4096 + 2560);
-    static_assert(kQueries * (D + 4) * 4 <= SB && kQueries * (D + 2) * 4 <= 2560 &&
+    static_assert(kQueries * (D + 4) * 4 <= SB && kQueries * (D + 4) * 4 <= 2560 &&
                   4096 + 2560 + 3 * 16 * kQueries * 4 <= NST * SB, "they fit");
 
     // ---------------------------------------------------------------- queries: on their way
@@ -158,11 +180,11 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const size_t v_bytes = (size_t)c.kv_heads * head_bytes;
     const uint8_t* const pages = c.pages + (size_t)kvh * head_bytes + lane * 16;
     int b_base = s_begin;                   // first tile of the batch below
-    int b_page = -1;                        // lane l: the page of tile b_base + l, and its scalars
-    float b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
+    int b_page = -1;                        // lane l: the page of tile b_base + l, and its scalars,
+    float b_ks = 0.f, b_vm = 0.f, b_ve = -INFINITY;     // the value scale as b_vm * 2^b_ve
     auto load_batch = [&]() {
         b_page = -1;
-        b_ks = 0.f, b_lv = -INFINITY, b_inv = 0.f;
+        b_ks = 0.f, b_vm = 0.f, b_ve = -INFINITY;
         const int s = b_base + lane;
         if (s < s_end) {
             const int p = __ldg(c.table + (size_t)row * c.row_pages + ((s * kTile) >> page_log2));
@@ -170,9 +192,7 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 const float* sc = c.scales + (size_t)p * 2 * c.kv_heads + kvh;
                 b_page = p;
                 b_ks = __ldg(sc);
-                const float vs = __ldg(sc + c.kv_heads);
-                b_lv = log2_of(vs);
-                b_inv = __frcp_rn(vs);
+                split_scale(__ldg(sc + c.kv_heads), b_vm, b_ve);
             } else if (c.status) {
                 atomicCAS(c.status, 0, c.arg_code);
             }
@@ -189,11 +209,11 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             const int src = fs - b_base;
             const int p = __shfl_sync(0xffffffffu, b_page, src);
             const float ks = __shfl_sync(0xffffffffu, b_ks, src);
-            const float lv = __shfl_sync(0xffffffffu, b_lv, src);
-            const float inv = __shfl_sync(0xffffffffu, b_inv, src);
+            const float vm = __shfl_sync(0xffffffffu, b_vm, src);
+            const float ve = __shfl_sync(0xffffffffu, b_ve, src);
             if (lane == 0)
                 *reinterpret_cast<float4*>(ring + fslot * SB + 2 * kTile * D) =
-                    make_float4(ks, lv, inv, 0.f);
+                    make_float4(ks, vm, ve, 0.f);
             const int k0 = fs * kTile;
             const uint8_t* kg = pages + (size_t)max(p, 0) * 2 * v_bytes +
                                 (size_t)((k0 & ((1 << page_log2) - 1)) * D);
@@ -262,9 +282,11 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     const int mask_from = __any_sync(0xffffffffu, t < nq && vis < vis_min) ? 0 : vis_min;
 
     // ---------------------------------------------------------------- the runs
-    float m = -INFINITY, l = 0.f, O[VJ][4];
+    // of query t: this lane's part of the weights' sum, and dims 2j, 2j + 1 of its D/8
+    Sum sum = {kNone, kNone, 0.f};
+    float O[VJ][2];
 #pragma unroll
-    for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
+    for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = 0.f;
     const int key_lo = 4 * (g & 1) + (g >> 1);      // sigma(g): the key of row g; row g + 8: + 8
     int slot = 0, run = 0, run_end = start_of(r_begin + 1);     // (run: of this warp's)
 
@@ -293,35 +315,40 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
         }
         uint32_t vv[4][D / 32];
         load_values<D>(st, g, t, vv);
-        // scores of key rows g, g + 8 and query t, the value scale folded in
+        // scores of key rows g, g + 8 and query t
         const float f = rf * meta.x;
-        float s0 = fmaf(fmaf(cf[1], 1.f / 2048.f, cf[0]), f, meta.y);
-        float s1 = fmaf(fmaf(cf[3], 1.f / 2048.f, cf[2]), f, meta.y);
-        const bool bad = !(meta.y > -INFINITY);
+        float s0 = fmaf(cf[1], 1.f / 2048.f, cf[0]) * f;
+        float s1 = fmaf(cf[3], 1.f / 2048.f, cf[2]) * f;
+        const bool bad = !(meta.z > -INFINITY);
         uint32_t poison = 0;                // keys of the tile with a NaN among their values
         if (bad || k0 + kTile > mask_from) {    // the prefix ends in this tile for some query
             if (bad || k0 + key_lo >= vis) s0 = -INFINITY;
             if (bad || k0 + key_lo + 8 >= vis) s1 = -INFINITY;
             if (mask_from < keys) poison = clear_nan<D>(vv, t);
         }
-        float mx = fmaxf(s0, s1);
-        if (__any_sync(0xffffffffu, mx > m + kLag)) {
+        float top = fmaxf(s0, s1);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float mn = fmaxf(m, mx);
-            const float r = m == mn ? 1.f : ex2(m - mn);        // m = -inf: 0
-            m = mn;
-            l *= r;
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = ceilf(top);                   // -inf: the query sees none of the tile
+        const float tv = top + meta.z;
+        const bool up_a = top > sum.a + kMost, up_e = tv > sum.e + kMost;
+        if (__any_sync(0xffffffffu, up_a || up_e)) {
+            const float an = up_a ? top : sum.a, en = up_e ? tv - kAhead : sum.e;
+            sum.l *= ex2(sum.a - an);
+            const float r = pow2(sum.e - en);
+            sum.a = an, sum.e = en;
 #pragma unroll
-            for (int j = 0; j < VJ; ++j) O[j][0] *= r, O[j][1] *= r, O[j][2] *= r, O[j][3] *= r;
+            for (int j = 0; j < VJ; ++j) O[j][0] *= r, O[j][1] *= r;
         }
-        const float mm = m == -INFINITY ? 0.f : m;
-        float p0 = ex2(s0 - mm), p1 = ex2(s1 - mm);
+        const float to_l = ex2(top - sum.a), to_o = meta.y * ex2(tv - sum.e);
+        const float zero = top == -INFINITY ? 0.f : top;
+        float p0 = ex2(s0 - zero), p1 = ex2(s1 - zero);
         if (poison) {
             if (s0 != -INFINITY && ((poison >> key_lo) & 1u)) p0 = NAN;
             if (s1 != -INFINITY && ((poison >> (key_lo + 8)) & 1u)) p1 = NAN;
         }
-        l = fmaf(p0 + p1, meta.z, l);
+        sum.l = fmaf(p0 + p1, to_l, sum.l);
+        p0 *= 32768.f, p1 *= 32768.f;       // (kWeight: most of fp16's range lies below 1)
         // the value product's operand: column 2t the leading bits, 2t + 1 the rest
         const float h0 = __half2float(__float2half_rn(p0)), h1 = __half2float(__float2half_rn(p1));
         const uint32_t b0 = transpose8(pack_h2(h0, (p0 - h0) * 2048.f));
@@ -333,32 +360,32 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 uint32_t a[4];
+                float of[4] = {0.f, 0.f, 0.f, 0.f};
                 h2x2_of(__byte_perm(vv[0][x], vv[1][x], y ? 0x7362 : 0x5140), a[0], a[1]);
                 h2x2_of(__byte_perm(vv[2][x], vv[3][x], y ? 0x7362 : 0x5140), a[2], a[3]);
-                mma_f16(O[2 * x + y], a, b0, b1);
+                mma_f16(of, a, b0, b1);
+                float(&to)[2] = O[2 * x + y];
+                to[0] = fmaf(fmaf(of[1], 1.f / 2048.f, of[0]), to_o, to[0]);
+                to[1] = fmaf(fmaf(of[3], 1.f / 2048.f, of[2]), to_o, to[1]);
             }
         }
         if (s + 1 == run_end) {             // the run's sums, and those of the subtrees it completes
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll
-            for (int j = 0; j < VJ; ++j) {
-                O[j][0] = fmaf(O[j][1], 1.f / 2048.f, O[j][0]);
-                O[j][2] = fmaf(O[j][3], 1.f / 2048.f, O[j][2]);
-            }
+            for (int o = 4; o < 32; o <<= 1) sum.l += __shfl_xor_sync(0xffffffffu, sum.l, o);
             const int at = t * D + g * (D / 8);
             int level = 0;
             for (; (run >> level) & 1; ++level) {
                 const float* const z = stack + level * run_floats;
                 if (t < nq) {
-                    float m1 = z[nq * D + t], l1 = z[nq * D + nq + t], fa, fb;
-                    join2(m1, l1, m, l, fa, fb);
-                    m = m1, l = l1;
+                    Sum left = {z[nq * D + t], z[nq * (D + 1) + t], z[nq * (D + 2) + t]};
+                    float fa, fb;
+                    join2(left, sum, fa, fb);
+                    sum = left;
 #pragma unroll
                     for (int j = 0; j < VJ; ++j) {
                         const float2 o = *reinterpret_cast<const float2*>(z + at + 2 * j);
                         O[j][0] = fmaf(fa, o.x, fb * O[j][0]);
-                        O[j][2] = fmaf(fa, o.y, fb * O[j][2]);
+                        O[j][1] = fmaf(fa, o.y, fb * O[j][1]);
                     }
                 }
             }
@@ -369,67 +396,76 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             if (t < nq) {
 #pragma unroll
                 for (int j = 0; j < VJ; ++j)
-                    *reinterpret_cast<float2*>(to + at + 2 * j) = make_float2(O[j][0], O[j][2]);
-                if (g == 0) to[nq * D + t] = m, to[nq * D + nq + t] = l;
+                    *reinterpret_cast<float2*>(to + at + 2 * j) = make_float2(O[j][0], O[j][1]);
+                if (g == 0)
+                    to[nq * D + t] = sum.a, to[nq * (D + 1) + t] = sum.e, to[nq * (D + 2) + t] = sum.l;
             }
 #pragma unroll
-            for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = O[j][2] = O[j][3] = 0.f;
-            m = -INFINITY, l = 0.f;
+            for (int j = 0; j < VJ; ++j) O[j][0] = O[j][1] = 0.f;
+            sum = {kNone, kNone, 0.f};
             ++run;
             run_end = start_of(r_begin + run + 1);
         }
     }
     if (tiles == 0 && wi == 0)              // no key: an empty sum
         for (int x = lane; x < run_floats; x += 32)
-            reinterpret_cast<float*>(ring)[x] = x >= nq * D && x < nq * D + nq ? -INFINITY : 0.f;
+            reinterpret_cast<float*>(ring)[x] = x >= nq * D && x < nq * (D + 2) ? kNone : 0.f;
     cp_wait<0>();
     __syncthreads();
 
     // ---------------------------------------------------------------- join
-    auto put = [&](int r, int d, float o, float lsum) {
+    auto put = [&](int r, int d, float o, const Sum& x) {   // o / l * 2^(e - a - kWeight)
+        const float by = x.e - x.a - kWeight, half = floorf(0.5f * by);
         out.p[(int64_t)row * out.row + (int64_t)(r / share) * out.token +
               (int64_t)(kvh * share + r % share) * D + d] =
-            from_f<TO>(lsum == 0.f ? 0.f : o / lsum);
+            from_f<TO>(x.l == 0.f ? 0.f : o / x.l * pow2(half) * pow2(by - half));
+    };
+    auto sum_at = [&](const float* z, int r) {
+        return Sum{z[nq * D + r], z[nq * (D + 1) + r], z[nq * (D + 2) + r]};
     };
     if (alive)
         for (int x = wi * 32 + lane; x < nq * D; x += unit_warps * 32) {
             const int r = x / D;
-            float mm[NW], ll[NW], o[NW];
+            Sum sm[NW];
+            float o[NW];
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const float* const z = reinterpret_cast<const float*>(first + w * (NST * SB));
-                mm[w] = -INFINITY, ll[w] = o[w] = 0.f;
-                if (w < busy) mm[w] = z[nq * D + r], ll[w] = z[nq * D + nq + r], o[w] = z[x];
+                sm[w] = {kNone, kNone, 0.f}, o[w] = 0.f;
+                if (w < busy) sm[w] = sum_at(z, r), o[w] = z[x];
             }
-            join_tree<NW>(mm, ll, o);
+            join_tree<NW>(sm, o, busy);
             if (ctas == 1) {
-                put(r, x - r * D, o[0], ll[0]);
+                put(r, x - r * D, o[0], sm[0]);
             } else {
                 g_o[x] = o[0];
-                if (x == r * D) g_o[nq * D + r] = mm[0], g_o[nq * D + nq + r] = ll[0];
+                if (x == r * D)
+                    g_o[nq * D + r] = sm[0].a, g_o[nq * (D + 1) + r] = sm[0].e,
+                    g_o[nq * (D + 2) + r] = sm[0].l;
             }
         }
     if (ctas == 1) return;
     cluster.sync();                                 // (CTAs without a run have exited)
-    for (int x = threadIdx.x; x < ctas * nq; x += NW * 32) {
-        const int k = x / nq, r = x - k * nq;
+    for (int x = threadIdx.x; x < ctas * 3 * nq; x += NW * 32) {
+        const int k = x / (3 * nq), r = x - k * 3 * nq;
         scratch[x] = *cluster.map_shared_rank(g_o + nq * D + r, k);
-        scratch[kMaxCtas * nq + x] = *cluster.map_shared_rank(g_o + nq * D + nq + r, k);
     }
     __syncthreads();
     for (int x = rank * NW * 32 + (int)threadIdx.x; x < nq * D; x += ctas * NW * 32) {
         const int r = x / D;
-        float mm[kMaxCtas], ll[kMaxCtas], o[kMaxCtas];
+        Sum sm[kMaxCtas];
+        float o[kMaxCtas];
 #pragma unroll
         for (int k = 0; k < kMaxCtas; ++k) {        // (the remote loads are all in flight at once)
-            mm[k] = -INFINITY, ll[k] = o[k] = 0.f;
+            sm[k] = {kNone, kNone, 0.f}, o[k] = 0.f;
             if (k < ctas) {
                 o[k] = *cluster.map_shared_rank(g_o + x, k);
-                mm[k] = scratch[k * nq + r], ll[k] = scratch[(kMaxCtas + k) * nq + r];
+                const float* const z = scratch + k * 3 * nq + r;
+                sm[k] = {z[0], z[nq], z[2 * nq]};
             }
         }
-        join_tree<kMaxCtas>(mm, ll, o);
-        put(r, x - r * D, o[0], ll[0]);
+        join_tree<kMaxCtas>(sm, o, ctas);
+        put(r, x - r * D, o[0], sm[0]);
     }
     cluster.sync();                                 // no CTA leaves while its memory is read
 }
@@ -481,7 +517,7 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
         return v;
     };
     auto smem = [&](int w) {
-        return (size_t)ring_bytes<D, 8>() + (size_t)8 * levels(w) * nq * (D + 2) * 4;
+        return (size_t)ring_bytes<D, 8>() + (size_t)8 * levels(w) * nq * (D + 4) * 4;
     };
     // Warps of a unit.  Short prefixes: as few as come near filling the machine, 12 an SM up to 512
     // keys, then 16 (a warp starts and ends in about four tiles' time: 256 rows x 8 heads x 64 of
