@@ -52,9 +52,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// order-preserving key of a float (no NaN), and back
+// order-preserving key of a float (no NaN; the zeros, which compare equal, have one), and back
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x + 0.f);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float float_of(uint32_t key) {
