@@ -9,6 +9,7 @@ constexpr int kMaxBeams = 64;
 
 // include/rlt.h: rlt_beam_select
 template <typename T>
+[[nodiscard]]
 cudaError_t launch_beam_select(const T* logits, const float* scores, const uint8_t* finished,
                                int eos, float temperature, int groups, int beams, int vocab,
                                int k, int32_t* parents, int32_t* tokens, float* new_scores,
@@ -27,6 +28,7 @@ struct ReorderSeg {
 };
 constexpr int kMaxSegs = 8;
 // Rows g*beams + i <- g*beams + parents[g*beams + i], every segment in one launch.
+[[nodiscard]]
 cudaError_t launch_reorder(const ReorderSeg* segs, int n_segs, const int32_t* parents, int groups,
                            int beams, cudaStream_t st);
 

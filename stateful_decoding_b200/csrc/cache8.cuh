@@ -31,6 +31,7 @@ struct Tok8 {
 
 // Tokens start[b] .. start[b]+counts[b]-1 of every row (counts null: n each).
 template <typename T>
+[[nodiscard]]
 cudaError_t launch_cache8_append(const Cache8& c, Tok8<const T> k, Tok8<const T> v,
                                  const int32_t* start, const int32_t* counts, int n,
                                  const Rope8& rope, cudaStream_t st);
@@ -38,12 +39,14 @@ cudaError_t launch_cache8_append(const Cache8& c, Tok8<const T> k, Tok8<const T>
 // q as a sum of S partial slabs (S = 1: q itself), of fp32; a row's prefix is
 // lens[b] + lens_add.
 template <typename TQ, typename TO>
+[[nodiscard]]
 cudaError_t launch_cache8_attend(const Cache8& c, Tok8<const TQ> q, int slabs, size_t slab,
                                  Tok8<TO> out, int heads, int n, const int32_t* lens,
                                  int lens_add, float scale, const Rope8& rope, cudaStream_t st);
 
 // The same, for n * heads / kv_heads <= 4.
 template <typename TQ, typename TO>
+[[nodiscard]]
 cudaError_t launch_cache8_decode(const Cache8& c, Tok8<const TQ> q, int slabs, size_t slab,
                                  Tok8<TO> out, int heads, int n, const int32_t* lens,
                                  int lens_add, float scale, const Rope8& rope, cudaStream_t st);

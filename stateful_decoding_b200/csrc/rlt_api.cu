@@ -807,6 +807,12 @@ static int launch_status() {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? RLT_OK : RLT_E_DEVICE;
 }
+// of a launcher that returns its error: what it refuses itself leaves no CUDA error behind
+static int launch_code(cudaError_t e) {
+    if (e == cudaSuccess) return RLT_OK;
+    cudaGetLastError();
+    return e == cudaErrorInvalidConfiguration ? RLT_E_UNSUPPORTED : RLT_E_DEVICE;
+}
 
 static rlt::RopeTab rope_of(rlt_state* s) {
     return rlt::RopeTab{s->rope_cs, s->rope_sn, s->m->dh / 2, s->T_cap};
@@ -925,9 +931,9 @@ static rlt::Rope8 mem8_rope(const rlt_state* s) {
 // kernel would walk every key tile twice for a mostly empty query tile.
 static constexpr int kEncTcMinPositions = 16;
 
+// An error leaves the positions as they were.
 template <typename T>
-static void encode_block(rlt_state* s, const int32_t* tok, int n, cudaStream_t st,
-                         bool tc_attn) {
+static int encode_block(rlt_state* s, const int32_t* tok, int n, cudaStream_t st, bool tc_attn) {
     using namespace rlt;
     rlt_model* m = s->m;
     const rlt_config& c = m->cfg;
@@ -993,10 +999,11 @@ static void encode_block(rlt_state* s, const int32_t* tok, int n, cudaStream_t s
             if (s->mem8) {                   // from the product in fp32: rotated and rounded once
                 launch_gemm<T>(Y, d, (const T*)m->wmem[g], d, s->QKV, 2 * d, nullptr, 0, R,
                                2 * d, d, kStoreF32, st);
-                launch_cache8_append<float>(mem8_of(s, g, 0, B),
-                                            {s->QKV, (int64_t)n * 2 * d, 2 * d},
-                                            {s->QKV + d, (int64_t)n * 2 * d, 2 * d}, s->pos_enc,
-                                            nullptr, n, mem8_rope(s), st);
+                if (int rc = launch_code(launch_cache8_append<float>(
+                        mem8_of(s, g, 0, B), {s->QKV, (int64_t)n * 2 * d, 2 * d},
+                        {s->QKV + d, (int64_t)n * 2 * d, 2 * d}, s->pos_enc, nullptr, n,
+                        mem8_rope(s), st)))
+                    return rc;
                 continue;
             }
             if constexpr (std::is_same<T, bf16>::value)
@@ -1014,6 +1021,7 @@ static void encode_block(rlt_state* s, const int32_t* tok, int n, cudaStream_t s
         }
     }
     launch_pos_add(s->pos_enc, B, n, st);
+    return launch_status();
 }
 
 extern "C" int rlt_encode(rlt_state* s, const int32_t* tokens, int n, void* stream) {
@@ -1038,14 +1046,14 @@ extern "C" int rlt_encode(rlt_state* s, const int32_t* tokens, int n, void* stre
                                           dev ? cudaMemcpyDeviceToDevice : cudaMemcpyHostToDevice,
                                           st);
         if (e != cudaSuccess) return RLT_E_DEVICE;
+        int rc;
         {
             ProfScope ps(s, n == 1 ? RLT_PROF_ENC1 : RLT_PROF_ENC, st,
                          s->prof ? enc_bytes(s, nb) : 0.0);
             const bool tc = n >= kEncTcMinPositions;      // by the call, not the block
-            if (m->cfg.dtype == RLT_DTYPE_BF16) encode_block<bf16>(s, s->tok, nb, st, tc);
-            else encode_block<float>(s, s->tok, nb, st, tc);
+            rc = m->cfg.dtype == RLT_DTYPE_BF16 ? encode_block<bf16>(s, s->tok, nb, st, tc)
+                                                : encode_block<float>(s, s->tok, nb, st, tc);
         }
-        int rc = launch_status();
         if (rc) return rc;
         // the next block's launch shapes (its longest key prefix) read the
         // host copy of the positions: advance it block by block
@@ -1063,9 +1071,10 @@ extern "C" int rlt_encode(rlt_state* s, const int32_t* tokens, int n, void* stre
 // b0, nb: the block runs rows b0 .. b0+nb-1 only (all rows by default).  A
 // row range keeps its own part of every scratch buffer (rows b0*n.. at each
 // buffer's widest pitch), so the ranges of one block can run concurrently.
+// An error leaves the positions as they were.
 template <typename T>
-static void step_block(rlt_state* s, int n, cudaStream_t st, bool merged_in = false,
-                       bool fuse_out = false, int b0 = 0, int nb = -1) {
+static int step_block(rlt_state* s, int n, cudaStream_t st, bool merged_in = false,
+                      bool fuse_out = false, int b0 = 0, int nb = -1) {
     using namespace rlt;
     rlt_model* m = s->m;
     const rlt_config& c = m->cfg;
@@ -1144,12 +1153,13 @@ static void step_block(rlt_state* s, int n, cudaStream_t st, bool merged_in = fa
         {
             ProfScope ps(s, RLT_PROF_XATTN, st, s->prof ? xattn_bytes(s, n, b0, B) : 0.0, l);
             bool done = s->mem8;
-            if (done)
-                launch_cache8_attend<float, T>(mem8_of(s, c.groups > 1 ? l : 0, b0, B),
-                                               {P, (int64_t)n * d, d}, np, slab,
-                                               {A, (int64_t)n * d, d}, h, n, pos_dec, n,
-                                               1.f / sqrtf((float)dh), mem8_rope(s), st);
-            else if constexpr (std::is_same<T, bf16>::value)
+            if (done) {
+                if (int rc = launch_code(launch_cache8_attend<float, T>(
+                        mem8_of(s, c.groups > 1 ? l : 0, b0, B), {P, (int64_t)n * d, d}, np, slab,
+                        {A, (int64_t)n * d, d}, h, n, pos_dec, n, 1.f / sqrtf((float)dh),
+                        mem8_rope(s), st)))
+                    return rc;
+            } else if constexpr (std::is_same<T, bf16>::value)
                 done = launch_attn_cross_proj(ProjIn{P, np, slab, d, rope_of(s)}, mem, s->mem_row,
                                               s->T_cap, pos_dec, A, B, n, h, dh, st);
             if (!done) {
@@ -1180,6 +1190,7 @@ static void step_block(rlt_state* s, int n, cudaStream_t st, bool merged_in = fa
         launch_set_state(z, nres ? P : nullptr, nres, slab, s_vec,
                          c.variant == 2 ? r_reg : nullptr, pos_dec, c.chunk, B, n, d,
                          /*bump=*/true, st);
+    return launch_status();
 }
 
 static int run_block(rlt_state* s, int n, cudaStream_t st) {
@@ -1187,12 +1198,12 @@ static int run_block(rlt_state* s, int n, cudaStream_t st) {
         if (s->h_pos_dec[b] + n > s->h_pos_enc[b]) return RLT_E_ORDER;
         if (s->h_pos_dec[b] + n > s->T_cap) return RLT_E_CAPACITY;
     }
+    int rc;
     {
         ProfScope ps(s, RLT_PROF_STEP, st, s->prof ? step_bytes(s, n) : 0.0);
-        if (s->m->cfg.dtype == RLT_DTYPE_BF16) step_block<bf16>(s, n, st);
-        else step_block<float>(s, n, st);
+        rc = s->m->cfg.dtype == RLT_DTYPE_BF16 ? step_block<bf16>(s, n, st)
+                                               : step_block<float>(s, n, st);
     }
-    int rc = launch_status();
     if (rc) return rc;
     for (int b = 0; b < s->B; ++b) s->h_pos_dec[b] += n;
     return RLT_OK;
@@ -1296,13 +1307,12 @@ static int run_graph(rlt_state* s, int n, cudaStream_t st) {
             for (int gi = 0; gi < G; ++gi) {
                 const int b0 = (int)((long)gi * s->B / G), b1 = (int)((long)(gi + 1) * s->B / G);
                 cudaStream_t sg = branch && gi > 0 ? s->aux[gi - 1] : st;
-                for (int k = 0; k < kGraphBlocks; ++k) {
+                for (int k = 0; k < kGraphBlocks && ok; ++k) {
                     s->prof_block = k;
                     const bool in = chain && k > 0, out = chain && k + 1 < kGraphBlocks;
-                    if (s->m->cfg.dtype == RLT_DTYPE_BF16)
-                        step_block<bf16>(s, n, sg, in, out, b0, b1 - b0);
-                    else
-                        step_block<float>(s, n, sg, in, out, b0, b1 - b0);
+                    ok = (s->m->cfg.dtype == RLT_DTYPE_BF16
+                              ? step_block<bf16>(s, n, sg, in, out, b0, b1 - b0)
+                              : step_block<float>(s, n, sg, in, out, b0, b1 - b0)) == RLT_OK;
                 }
             }
             if (branch)
@@ -1310,7 +1320,7 @@ static int run_graph(rlt_state* s, int n, cudaStream_t st) {
                     cudaEventRecord(evs[k], s->aux[k - 1]);
                     cudaStreamWaitEvent(st, evs[k], 0);
                 }
-            ok = cudaStreamEndCapture(st, &g) == cudaSuccess && g != nullptr;
+            ok = cudaStreamEndCapture(st, &g) == cudaSuccess && g != nullptr && ok;
         }
         for (auto& ev : evs)
             if (ev) cudaEventDestroy(ev);
@@ -1641,10 +1651,7 @@ static int reorder_rows(rlt_state* s, const int32_t* parents, int beams, int sha
         seg[n++] = {(uint8_t*)s->mem8_scales, srow, s->B * srow, sc, s->pos_enc, shared, longest,
                     c.groups, kMem8Page};
     }
-    const cudaError_t e = rlt::launch_reorder(seg, n, parents, s->B / beams, beams, st);
-    if (e == cudaSuccess) return RLT_OK;
-    cudaGetLastError();
-    return e == cudaErrorInvalidConfiguration ? RLT_E_UNSUPPORTED : RLT_E_DEVICE;
+    return launch_code(rlt::launch_reorder(seg, n, parents, s->B / beams, beams, st));
 }
 
 extern "C" int rlt_state_reorder(rlt_state* s, const int32_t* parents, int beams, int shared,
@@ -1693,13 +1700,11 @@ extern "C" int rlt_beam_step(rlt_state* s, float* scores, uint8_t* finished, int
     readout_logits(s, s->logits, st);
     int rc = launch_status();
     if (rc) return rc;
-    if (rlt::launch_beam_select<float>(s->logits, scores, finished, eos, temperature,
-                                       s->B / beams, beams, c.vocab, beams, parents, tokens,
-                                       s->beam_scores, finished ? s->beam_fin : nullptr,
-                                       st) != cudaSuccess) {
-        cudaGetLastError();
-        return RLT_E_DEVICE;
-    }
+    rc = launch_code(rlt::launch_beam_select<float>(s->logits, scores, finished, eos, temperature,
+                                                    s->B / beams, beams, c.vocab, beams, parents,
+                                                    tokens, s->beam_scores,
+                                                    finished ? s->beam_fin : nullptr, st));
+    if (rc) return rc;
     if (cudaMemcpyAsync(scores, s->beam_scores, B * 4, cudaMemcpyDeviceToDevice, st) ||
         (finished && cudaMemcpyAsync(finished, s->beam_fin, B, cudaMemcpyDeviceToDevice, st)))
         return RLT_E_DEVICE;
