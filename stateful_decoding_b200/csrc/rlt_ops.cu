@@ -118,7 +118,8 @@ extern "C" int rlt_cache8_append(const rlt_cache8* cache, int dtype, const void*
     const int64_t wide = (int64_t)cache->kv_heads * cache->dh;
     if (!aligned16(k) || !aligned16(v) || !pitch_ok(k_token, wide, n, elt) ||
         !pitch_ok(v_token, wide, n, elt) || !pitch_ok(k_row, wide, cache->rows, elt) ||
-        !pitch_ok(v_row, wide, cache->rows, elt))
+        !pitch_ok(v_row, wide, cache->rows, elt) || ((uintptr_t)start & 3) ||
+        ((uintptr_t)counts & 3))
         return RLT_E_ARG;
     if (device_of(k) != dev || device_of(v) != dev || device_of(start) != dev ||
         (counts && device_of(counts) != dev))
@@ -154,7 +155,7 @@ extern "C" int rlt_cache8_attend(const rlt_cache8* cache, int dtype, const void*
     const int64_t wide = (int64_t)heads * cache->dh;
     if (!aligned16(q) || !aligned16(out) || !pitch_ok(q_token, wide, n, elt) ||
         !pitch_ok(out_token, wide, n, elt) || !pitch_ok(q_row, wide, cache->rows, elt) ||
-        !pitch_ok(out_row, wide, cache->rows, elt))
+        !pitch_ok(out_row, wide, cache->rows, elt) || ((uintptr_t)lens & 3))
         return RLT_E_ARG;
     if (device_of(q) != dev || device_of(out) != dev || device_of(lens) != dev) return RLT_E_ARG;
     OnDevice on(dev);
