@@ -479,7 +479,8 @@ int rlt_rows_reorder(void* rows, const int32_t* parents, int groups, int beams, 
  * hold the same C^E and M at positions 1 .. shared (a common prompt; 0: none
  * promised), which are not moved.  parents: int32 [batch], host or device; on
  * the host an entry outside [0, beams) is RLT_E_ARG, on the device it leaves
- * its row as it was.  e_t of consumed positions stay where they are. */
+ * its row as it was (RLT_E_ARG off 4 bytes, or on another device than the
+ * model's).  e_t of consumed positions stay where they are. */
 int rlt_state_reorder(rlt_state* state, const int32_t* parents, int beams, int shared,
                       void* stream);
 
@@ -491,8 +492,8 @@ int rlt_state_reorder(rlt_state* state, const int32_t* parents, int beams, int s
  * tokens (int32 [batch]) receive what was chosen: the caller keeps them, step
  * by step, to read the sequences back.  A finished beam goes on with eos at an
  * unchanged score.  A search starts with all rows past the prompt, scores 0
- * for its first row and -infinity for the others.  All four arrays are device
- * memory.  The first call allocates 5 * batch bytes in the state.  RLT_E_ORDER
+ * for its first row and -infinity for the others.  All four arrays are memory
+ * of the model's device, aligned to their elements (else RLT_E_ARG).  The first call allocates 5 * batch bytes in the state.  RLT_E_ORDER
  * when a row has encoded tokens not yet consumed, RLT_E_CAPACITY at max_len;
  * argument limits as rlt_beam_select's. */
 int rlt_beam_step(rlt_state* state, float* scores, uint8_t* finished, int eos, float temperature,

@@ -802,6 +802,15 @@ static bool is_device_ptr(const void* p) {
     }
     return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
 }
+// memory that a kernel on `device` can read as 32-bit words
+static bool is_words_on(const void* p, int device) {
+    cudaPointerAttributes a;
+    if (((uintptr_t)p & 3) || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == device);
+}
 
 static int launch_status() {
     cudaError_t e = cudaGetLastError();
@@ -1669,6 +1678,8 @@ extern "C" int rlt_state_reorder(rlt_state* s, const int32_t* parents, int beams
             cudaStreamSynchronize(st))      // the caller may reuse its array
             return RLT_E_DEVICE;
         p = s->rows;
+    } else if (!is_words_on(parents, s->m->device)) {
+        return RLT_E_ARG;
     }
     return reorder_rows(s, p, beams, shared, st);
 }
@@ -1688,9 +1699,10 @@ extern "C" int rlt_beam_step(rlt_state* s, float* scores, uint8_t* finished, int
         if (s->h_pos_enc[b] >= s->T_cap) return RLT_E_CAPACITY;
     }
     if (cudaSetDevice(s->m->device) != cudaSuccess) return RLT_E_DEVICE;
-    if (!is_device_ptr(scores) || !is_device_ptr(parents) || !is_device_ptr(tokens) ||
-        (finished && !is_device_ptr(finished)))
-        return RLT_E_ARG;
+    const int dev = s->m->device;
+    if (!is_words_on(scores, dev) || !is_words_on(parents, dev) || !is_words_on(tokens, dev) ||
+        (finished && !is_words_on((const void*)((uintptr_t)finished & ~(uintptr_t)3), dev)))
+        return RLT_E_ARG;                    // (bytes of finished: any alignment)
     if (!s->beam_scores)
         if (int rc = salloc(s, (void**)&s->beam_scores, (size_t)s->B * 4)) return rc;
     if (!s->beam_fin)
