@@ -50,6 +50,7 @@ k_reorder(const __grid_constant__ Segs segs, const int32_t* __restrict__ parents
     if (sg.pos) {                   // a group's rows sit at one position
         const int64_t last = ((int64_t)__ldg(sg.pos + row0) + sg.page - 1) / sg.page * sg.unit;
         if (first + (x + 1) * (int64_t)sizeof(V) > last) return;
+        if (sg.from && first + x * (int64_t)sizeof(V) < __ldg(sg.from + row0) * sg.unit) return;
     }
     uint8_t* base = sg.base + (int64_t)row0 * sg.row + plane * sg.plane + first +
                     x * (int64_t)sizeof(V);

@@ -1646,7 +1646,7 @@ static int reorder_rows(rlt_state* s, const int32_t* parents, int beams, int sha
     const int64_t ring = (int64_t)s->ring_row * elt;
     seg[n++] = {(uint8_t*)s->ring, ring, 0, ring, nullptr, 0, 1, 1, 1};
     // e_t of the positions that transitions still have to merge
-    seg[n++] = {(uint8_t*)s->e, T * d * 4, 0, d * 4, s->pos_enc, consumed, longest, 1, 1};
+    seg[n++] = {(uint8_t*)s->e, T * d * 4, 0, d * 4, s->pos_enc, consumed, longest, 1, 1, s->pos_dec};
     seg[n++] = {(uint8_t*)s->enc, (int64_t)s->enc_row * elt, T * dh * elt, dh * elt, s->pos_enc,
                 shared, longest, 2 * c.n_enc * c.heads, 1};
     if (c.n_dec > 0 && !s->mem8) {
