@@ -71,11 +71,12 @@ int check_cache(const rlt_cache8* c, int* dev) {
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return RLT_E_UNSUPPORTED;
     if (c->dh != 64 && c->dh != 128) return RLT_E_UNSUPPORTED;
     if ((int64_t)c->row_pages * c->page > kMostTokens || c->kv_heads > (1 << 20)) return RLT_E_UNSUPPORTED;
-    if (!c->pages || !c->scales || !c->table || !aligned16(c->pages) ||
+    const bool some = c->rows > 0;              // (a table of no rows may have no address)
+    if (!c->pages || !c->scales || (some && !c->table) || !aligned16(c->pages) ||
         ((uintptr_t)c->scales & 3) || ((uintptr_t)c->table & 3) || ((uintptr_t)c->status & 3))
         return RLT_E_ARG;
     *dev = device_of(c->pages);
-    if (*dev < 0 || device_of(c->scales) != *dev || device_of(c->table) != *dev ||
+    if (*dev < 0 || device_of(c->scales) != *dev || (some && device_of(c->table) != *dev) ||
         (c->status && device_of(c->status) != *dev))
         return RLT_E_ARG;
     return RLT_OK;

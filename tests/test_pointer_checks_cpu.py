@@ -29,7 +29,12 @@ ref = ctypes.byref(cache)
 append = lambda start=at, counts=at, n=1: sd._lib.rlt_cache8_append(
     ref, 0, at, 128, 128, at, 128, 128, start, counts, n, None, None)
 attend = lambda lens=at: sd._lib.rlt_cache8_attend(ref, 0, at, 128, 128, at, 128, 128, 2, 1, lens, 0.125, None, None)
-got = {"append": append(), "append all": append(counts=None), "attend": attend()}
+cache.rows, cache.table = 0, None
+got = {"append no rows": append(), "attend no rows": attend()}
+cache.rows = 2
+got.update({"append no table": append(), "attend no table": attend()})
+cache.table = at
+got |= {"append": append(), "append all": append(counts=None), "attend": attend()}
 for off in (1, 2, 3, 4, 6):
     got["start %d" % off] = append(start=at + off)
     got["counts %d" % off] = append(counts=at + off)
@@ -63,3 +68,9 @@ def test_aligned_addresses_pass(answers):
 def test_lengths_off_four_bytes_are_refused(answers, what):
     for off in (1, 2, 3, 6):
         assert answers["%s %d" % (what, off)] == RLT_E_ARG, (what, off)
+
+
+def test_no_rows_need_no_table(answers):
+    """A call for 0 rows does nothing; an empty table has no address."""
+    assert answers["append no rows"] == answers["attend no rows"] == 0
+    assert answers["append no table"] == answers["attend no table"] == RLT_E_ARG
