@@ -51,7 +51,9 @@ struct OnDevice {
 int rc_of(cudaError_t e) {
     if (e == cudaSuccess) return RLT_OK;
     cudaGetLastError();
-    return e == cudaErrorInvalidConfiguration ? RLT_E_UNSUPPORTED : RLT_E_DEVICE;
+    return e == cudaErrorInvalidConfiguration     ? RLT_E_UNSUPPORTED
+           : e == cudaErrorInvalidResourceHandle ? RLT_E_ARG      // a stream of another device
+                                                 : RLT_E_DEVICE;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }

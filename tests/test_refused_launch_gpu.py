@@ -26,6 +26,7 @@ model = sd.Model(ri.write_blob(cfg, ri.generate_weights(cfg, seed=7, std=0.02), 
 tok = np.random.default_rng(1).integers(0, cfg.vocab, (2, 20)).astype(np.int32)
 st = sd.State(model, 2, 64, mem8=True)
 side = torch.cuda.Stream()
+rows = torch.zeros(2, 16, dtype=torch.uint8, device="cuda")
 i32 = lambda: torch.zeros(2, dtype=torch.int32, device="cuda")
 lp = np.zeros((2, 20), np.float32)
 calls = {
@@ -35,6 +36,7 @@ calls = {
     "prefill by graph": lambda: sd.rlt_prefill(st.handle, 20, stream=side),
     "replay": lambda: sd.rlt_replay_logprobs(st.handle, tok, 20, lp, 1.0),
     "packed": lambda: sd.rlt_prefill_packed(st.handle, tok, np.eye(2, 20, dtype=np.uint8), 20),
+    "reorder": lambda: sd._lib.rlt_rows_reorder(rows.data_ptr(), i32().data_ptr(), 1, 2, 16, 1, 0, 0, 16, None),
     "beam": lambda: sd.rlt_beam_step(st.handle, torch.zeros(2, device="cuda"), None, -1, 1.0, 2, 0, i32(), i32()),
 }
 got = {}
@@ -62,9 +64,10 @@ def _symbol(library, pattern):
     return found[0]
 
 
-def _run(library, tmp_path, pattern, dtype, calls):
+def _run(library, tmp_path, pattern, dtype, calls, error=9):
     src, so = tmp_path / "refuse.c", tmp_path / "refuse.so"
-    src.write_text('int refuse(void) __asm__("%s");\nint refuse(void) { return 9; }\n' % _symbol(library, pattern))
+    src.write_text('int refuse(void) __asm__("%s");\nint refuse(void) { return %d; }\n' % (
+        _symbol(library, pattern), error))
     subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
     env = dict(os.environ, LD_PRELOAD=str(so), PYTHONPATH=ROOT)
     r = subprocess.run([sys.executable, "-c", CHILD, dtype, calls], capture_output=True, text=True, cwd=ROOT, env=env,
@@ -73,7 +76,7 @@ def _run(library, tmp_path, pattern, dtype, calls):
     return json.loads(r.stdout.strip().splitlines()[-1])
 
 
-UNSUPPORTED = -8
+UNSUPPORTED, ARG, DEVICE = -8, -1, -6
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -97,3 +100,10 @@ def test_a_refused_attention_is_the_calls_error(library, tmp_path, dtype, patter
 def test_a_refused_selection_is_the_calls_error(library, tmp_path):
     got = _run(library, tmp_path, r"launch_beam_selectIfE", "fp32", "beam")
     assert got["beam"] == [UNSUPPORTED, [0, 0], [0, 0]]
+
+
+@pytest.mark.parametrize("error,code", [(400, ARG), (9, UNSUPPORTED), (719, DEVICE)])
+def test_a_stream_of_another_device_is_an_argument_error(library, tmp_path, error, code):
+    """The launch then fails with cudaErrorInvalidResourceHandle (400); other errors are what they were."""
+    got = _run(library, tmp_path, r"14launch_reorderE", "fp32", "reorder", error)
+    assert got["reorder"][0] == code
