@@ -161,6 +161,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     __shared__ float s_red[4][QT], s_red2[4][QT];
     __shared__ __align__(8) uint64_t s_k[2], s_v[2], s_s[2], s_w[2], s_o[2];   // K, V, S, w there; O done
     __shared__ __align__(8) uint64_t s_there[4];                              // a tile's s_meta
+    __shared__ __align__(8) uint64_t s_end;             // all products issued, after a wait gave up
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -176,6 +177,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             tc::mbar_init(&s_o[b], 1);
         }
         for (int b = 0; b < 4; ++b) tc::mbar_init(&s_there[b], kConvert);
+        tc::mbar_init(&s_end, 1);
         s_abort = 0;
         tc::fence_mbar_init();
     }
@@ -653,7 +655,13 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     }
     __syncthreads();
     tc::fence_after_sync();
-    if (s_abort && tid == 0) say(c.late_code);              // a bounded wait gave up
+    if (s_abort) {                          // a bounded wait gave up
+        if (tid == 0) say(c.late_code);
+        if (tid == 32 * (kWarps + kConvert)) {      // products under way end before their memory goes
+            tc::mma_commit(&s_end);
+            tc::mbar_wait(&s_end, 0, 1u << 22);
+        }
+    }
 
     // ---------------------------------------------------------------- join
     // l over the 128 keys, then this CTA's O [query][D], m, l
