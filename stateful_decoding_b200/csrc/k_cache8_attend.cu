@@ -66,7 +66,7 @@ constexpr int threads_of(int N) { return 32 * (weigh_warps(N) + kConvert + 1); }
 constexpr int kKeys = 128;              // of a tile
 constexpr int kKeysPerCta = 2048;
 constexpr int64_t kLongKeys = 32768;    // from here on
-constexpr int kMaxCtas = 16;            // CTAs (one cluster) share a prefix, below
+constexpr int kMaxCtas = 16;            // of a prefix: a cluster's most
 // Larger clusters wait for as many SMs of one group of SMs to be free at once: 16 rows of 20011 keys
 // x 4 key heads take 135, 149, 165, 214 us with at most 2, 4, 6, 8.  Fewer CTAs serve a few rows
 // worse: a row's own time grows (103 to 20011 keys: 133, 121, 118, 127 us).
@@ -144,6 +144,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
     constexpr int QT = N / PARTS;               // query vectors of a tile
     constexpr int kWarps = weigh_warps(N), kWeigh = 32 * kWarps, kThreads = threads_of(N);
     constexpr int NC = 4 * N / kWarps, NQ = NC / PARTS;     // a weighing thread's columns, and queries
+    static_assert(NC == 8 || NC == 16, "a load of scores");
     constexpr int NL = D / 32;                  // a thread's 16-byte loads of K (and of V) per tile
     constexpr uint32_t kCols = 4 * N;           // tensor memory: S twice, then O (of two tiles)
     extern __shared__ uint8_t raw[];
@@ -510,8 +511,7 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             {
                 float cf[NC];
                 if constexpr (NC == 8) tmem_ld8(S + b * N, cf);
-                else if constexpr (NC == 16) tc::tmem_ld16(S + b * N, cf);
-                else tc::tmem_ld32(S + b * N, cf);
+                else tc::tmem_ld16(S + b * N, cf);
 #pragma unroll
                 for (int j = 0; j < NQ; ++j)
                     x[j] = PARTS == 2 ? fmaf(cf[PARTS * j + PARTS - 1], 1.f / 2048.f, cf[PARTS * j])
