@@ -35,19 +35,21 @@
 // a and d are raised only when a score or a weight passes them by 2^8 (one
 // barrier vote per tile); then the columns' maxima are found and O rescaled.
 //
-// 16 rows of 103 to 20011 keys x 4 key heads x 32 queries (165 MB) take 111-115 us against
+// 16 rows of 103 to 20011 keys x 4 key heads x 32 queries (165 MB) take 112-114 us against
 // 26 of the bytes: a tile takes about 2300 cycles (its conversion, its two products and
 // its weighing are some 1400 each and wait for one another), a CTA's start and end
-// about 17000.  (Sixteen queries a warp through m16n8k16 products, every key converted
-// by each warp: 174 us; one stage, two CTAs an SM: 121.)
+// about 17000.  fp32 types: 165 us.  (Sixteen queries a warp through m16n8k16 products, every key converted
+// by each warp: 174 us; one stage, two CTAs an SM: 121.)  One register budget serves all
+// three kinds of warps: at head size 128 a thread spills 88 to 140 bytes at 32 columns (96
+// registers) and 344 to 484 at 64 (72 registers).
 //
 // Split.  The prefix of a (row, key head) is cut into runs of 2048 keys, or 4
 // longer ones (16 from 32768 keys on), for a CTA each, a function of that
 // prefix alone; they join through the cluster's distributed shared memory in
 // run order: no scratch, no atomics, and the same bits for a row whatever batch
-// or capacity it sits in.
+// or capacity it sits in.  The grid is the capacity's, though: CTAs past a row's own
+// take tensor memory, read its length and leave.
 #include <cooperative_groups.h>
-#include <float.h>
 
 #include <algorithm>
 
@@ -60,7 +62,8 @@ namespace {
 
 constexpr int kConvert = 8;             // warps that convert
 // warps that weigh, four to a set of columns; one more issues (16 for 64 columns: 16 rows of 103 to
-// 20011 keys x 4 key heads x 128 queries take 294 us, 318 with 8; for 32 columns 135 and 122)
+// 20011 keys x 4 key heads x 128 queries took 294 us, now 277, and 318 with 8; for 32 columns 135 and
+// 122)
 constexpr int weigh_warps(int N) { return N == 64 ? 16 : 8; }
 constexpr int threads_of(int N) { return 32 * (weigh_warps(N) + kConvert + 1); }
 constexpr int kKeys = 128;              // of a tile
@@ -129,6 +132,26 @@ __device__ __forceinline__ uint32_t key_of(float x) {   // order-preserving
 }
 __device__ __forceinline__ float float_of(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// two fp32 values in one register pair: one instruction for both
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 template <int D, int N>
@@ -428,9 +451,9 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 poison = __reduce_or_sync(0xffffffffu, poison);
             }
             if (lane == 0) {
-                float vm, ve;
-                split_scale(vs, vm, ve);
-                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, vs, vm > 1.f ? ve + 1.f : ve, 0.f)
+                // log2 vs, rounded up
+                const int up = (int)((__float_as_uint(vs) + 0x7fffffu) >> 23) - 127;
+                s_meta[i & 3][cw] = vs > 0.f ? make_float4(ks, vs, (float)up, 0.f)
                                          : make_float4(0.f, 0.f, -INFINITY, 0.f);
                 s_poison[i & 3][cw] = poison;
             }
@@ -524,10 +547,12 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                 const float4 rf = reinterpret_cast<const float4*>(s_rf)[at];
                 const float4 mq = reinterpret_cast<const float4*>(s_m)[at];
                 const float4 room = reinterpret_cast<const float4*>(s_room)[at];
-                x[j] = fmaf(x[j], rf.x * meta.x, -mq.x);
-                x[j + 1] = fmaf(x[j + 1], rf.y * meta.x, -mq.y);
-                x[j + 2] = fmaf(x[j + 2], rf.z * meta.x, -mq.z);
-                x[j + 3] = fmaf(x[j + 3], rf.w * meta.x, -mq.w);
+                const uint64_t k2 = pair(meta.x, meta.x);
+                unpair(fma2(pair(x[j], x[j + 1]), mul2(pair(rf.x, rf.y), k2), pair(-mq.x, -mq.y)),
+                       x[j], x[j + 1]);
+                unpair(fma2(pair(x[j + 2], x[j + 3]), mul2(pair(rf.z, rf.w), k2),
+                            pair(-mq.z, -mq.w)),
+                       x[j + 2], x[j + 3]);
                 if (tail) {
                     const int4 vis = reinterpret_cast<const int4*>(s_vis)[at];
                     if (k0 + key >= vis.x) x[j] = -INFINITY;
@@ -572,8 +597,8 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
                         // (the largest score itself: a key that dwarfs the others weighs exactly 1)
                         const float up = none ? top : fmaxf(0.f, top);
                         const float left = s_room[tid] - kLag - up;         // d, were it to stay a + d
-                        // -118: 2^(kUp - d) stays finite; nothing but scales below 2^-110 comes near
-                        float d = fmaxf(-118.f, ceilf(top2 - up));
+                        // -105: p 2^(kUp - d) stays finite; scales of zeros alone lie below
+                        float d = fmaxf(-105.f, ceilf(top2 - up));
                         if (!none) d = fmaxf(d, ceilf(left));
                         s_up[tid] = up;
                         s_f[tid] = none ? 1.f : ex2(-up);
@@ -611,31 +636,30 @@ k_cache8_attend(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
 #pragma unroll
             for (int j = 0; j < NC; j += 8) {               // weights, 8 columns at a time
                 uint32_t w[4];
-                float f[8 / PARTS];                         // (finite: a weight of 0 stays 0)
 #pragma unroll
                 for (int z = 0; z < 8 / PARTS; z += 4) {
                     const float4 g = reinterpret_cast<const float4*>(s_g)[(part * NQ + j / PARTS + z) / 4];
-                    f[z] = fminf(meta.y * g.x, FLT_MAX);
-                    f[z + 1] = fminf(meta.y * g.y, FLT_MAX);
-                    f[z + 2] = fminf(meta.y * g.z, FLT_MAX);
-                    f[z + 3] = fminf(meta.y * g.w, FLT_MAX);
-                }
+                    float p[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    float p[2];
-#pragma unroll
-                    for (int e = 0; e < (PARTS == 2 ? 1 : 2); ++e) {
-                        const int at = PARTS == 2 ? z : 2 * z + e, qi = j / PARTS + at;
+                    for (int e = 0; e < 4; ++e) {
+                        const int qi = j / PARTS + z + e;
                         p[e] = ex2(x[qi]);
                         if (poisoned && x[qi] != -INFINITY) p[e] = NAN;
                         l[qi] += p[e];
-                        p[e] *= f[at];
                     }
+                    // (finite factors: a weight of 0 stays 0)
+                    const uint64_t v2 = pair(meta.y, meta.y);
+                    unpair(mul2(mul2(pair(p[0], p[1]), pair(g.x, g.y)), v2), p[0], p[1]);
+                    unpair(mul2(mul2(pair(p[2], p[3]), pair(g.z, g.w)), v2), p[2], p[3]);
                     if (PARTS == 2) {
-                        const float h = __half2float(__float2half_rn(p[0]));
-                        w[z] = pack_h2(h, (p[0] - h) * 2048.f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float h = __half2float(__float2half_rn(p[e]));
+                            w[e] = pack_h2(h, (p[e] - h) * 2048.f);
+                        }
                     } else {
-                        w[z] = pack_h2(p[0], p[PARTS == 2 ? 0 : 1]);
+                        w[z / 2] = pack_h2(p[0], p[1]);
+                        w[z / 2 + 1] = pack_h2(p[2], p[3]);
                     }
                 }
                 const int ch = (part * NC + j) >> 3;

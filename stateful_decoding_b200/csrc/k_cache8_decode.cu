@@ -33,12 +33,12 @@
 // through distributed shared memory: no scratch, no atomics.
 //
 // Bound by HBM for long batches: 64 rows x 16 heads x 4.3k keys x 128 (1.14 GB) take
-// 204-219 us from one B200 to another, 5.2-5.6 TB/s, 0.8-0.87 of the copy rate; 16 warps an SM,
-// about 350 instructions a 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64 take
-// 21 us (floor 5.5): their warps start and end, four dependent loads deep, for a few tiles
-// each (1 us of it the tiles' largest scores, three shuffles each).  One row of 131072 keys x 8
-// heads takes 87 us (floor 42): 16 CTAs a head are a cluster's limit, and they pack on
-// half of the SMs.  (Products added in pairs by packed fp32 instructions: 220 and 91 us.)
+// 204-216 us from one B200 to another, 5.3-5.6 TB/s, 0.82-0.87 of the copy rate; 16 warps
+// an SM, about 350 instructions a 4 KB tile.  256 rows x 8 heads of at most 256 keys x 64
+// take 21 us (floor 5.5): their warps start and end, four dependent loads deep, for a few
+// tiles each.  One row of 131072 keys x 8 heads takes 86 us (floor 42): 16 CTAs a head are
+// a cluster's limit, and they pack on half of the SMs.  (Products added in pairs by packed
+// fp32 instructions: 220 and 91 us.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -80,6 +80,12 @@ __device__ __forceinline__ float pow2(float x) {
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// the largest of a warp's values (one instruction; three shuffles for 8 lanes each take longer: 256
+// rows x 8 heads of 256 keys 21.2 us, 20.8 with this)
+__device__ __forceinline__ float warp_max(float x) {
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
+    return x;
 }
 // Sums over some keys: l of weights, in units of 2^a; o of weighted values (one a dim), in units of 2^e
 struct Sum {
@@ -326,9 +332,17 @@ k_cache8_decode(Cache8 c, int page_log2, QIn<TQ> q, Tok8<TO> out, int share, int
             if (bad || k0 + key_lo + 8 >= vis) s1 = -INFINITY;
             if (mask_from < keys) poison = clear_nan<D>(vv, t);
         }
-        float top = fmaxf(s0, s1);
+        float top = fmaxf(s0, s1);          // of query t's 8 lanes
+        if (nq == 1) {
+            top = warp_max(t ? -INFINITY : top);
+        } else if (nq == 2) {
+            const float of0 = warp_max(t == 0 ? top : -INFINITY);
+            const float of1 = warp_max(t == 1 ? top : -INFINITY);
+            top = t ? of1 : of0;
+        } else {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
         top = ceilf(top);                   // -inf: the query sees none of the tile
         const float tv = top + meta.z;
         const bool up_a = top > sum.a + kMost, up_e = tv > sum.e + kMost;
@@ -519,10 +533,10 @@ cudaError_t plan(const Cache8& c, const QIn<TQ>& q, const Tok8<TO>& out, int sha
     auto smem = [&](int w) {
         return (size_t)ring_bytes<D, 8>() + (size_t)8 * levels(w) * nq * (D + 4) * 4;
     };
-    // Warps of a unit.  Short prefixes: as few as come near filling the machine, 12 an SM up to 512
+    // Warps of a unit, by the capacity (lengths are on the device).  Short prefixes: as few as come near filling the machine, 12 an SM up to 512
     // keys, then 16 (a warp starts and ends in about four tiles' time: 256 rows x 8 heads x 64 of
     // 256 keys take 21 us with one warp, 25 with two; 128 rows x 16 heads x 128 of 1024 keys 100
-    // and 96).  Longer ones: 8 (48 rows x 16 heads of 2k to 8k keys: 234 us with four, 202
+    // and 96: two measurements, nothing between them).  Longer ones: 8 (48 rows x 16 heads of 2k to 8k keys: 234 us with four, 202
     // with 8), and more as long as all run at once (9 rows x 16 heads of 4.3k keys: 50 us with 32,
     // in two turns, 37 with 16).  More also where the subtrees leave no room for two CTAs an SM.
     int w = std::min(cap <= 1024 ? 1 : 8, runs);
