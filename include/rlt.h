@@ -361,8 +361,8 @@ int rlt_debug_set_positions(rlt_state* state, int row, int32_t pos_enc, int32_t 
  * query without a rotation gives 0); RLT_E_TIMEOUT, a bounded wait inside
  * attend gave up (its output is then undefined).  The caller zeroes it.
  * Table entries of blocks past a row's length are not read.  Pages may be
- * shared between rows for reading; a page that two rows of one append write
- * is undefined.  Attention is laid out for the table's width, since lengths are
+ * shared between rows for reading; a page that two rows of one append write, or
+ * one row twice, is undefined.  Attention is laid out for the table's width, since lengths are
  * on the device: 64 rows of 480 keys, 4 key heads x 8 queries of 128, take 31 us in
  * a table of 512 positions, 66 below 32768 and 195 from there on (one query a
  * key head, 16 of them: 43, 53, and 84 at 131072), so pass one no wider than the
