@@ -56,11 +56,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // V values of T_ in pieces of at most 16 bytes; piece p of a thread is `pitch` behind piece p - 1,
 // so that neighbouring threads' pieces are neighbours
@@ -304,12 +299,16 @@ k_cache8_append(Cache8 c, Tok8<const T_> k, Tok8<const T_> v, const int32_t* __r
 #pragma unroll
                     for (int e = V * q; e < V * q + V; e += 2) {
                         // products and sums rounded one by one, not contracted: the bytes do
-                        // not depend on how a compiler fuses the pair
+                        // not depend on how a compiler fuses the pair (packed sums it does fuse)
                         const uint64_t x1 = pair(x[e], x[e + 1]), x2 = pair(y[e], y[e + 1]);
                         const uint64_t c1 = pair(cs[e], cs[e + 1]), s1 = pair(sn[e], sn[e + 1]);
-                        const uint64_t n1 = pair(-sn[e], -sn[e + 1]);
-                        unpair(add2(mul2(x1, c1), mul2(x2, n1)), x[e], x[e + 1]);
-                        unpair(add2(mul2(x2, c1), mul2(x1, s1)), y[e], y[e + 1]);
+                        float a[2], b[2], c[2], d[2];
+                        unpair(mul2(x1, c1), a[0], a[1]);
+                        unpair(mul2(x2, s1), b[0], b[1]);
+                        unpair(mul2(x2, c1), c[0], c[1]);
+                        unpair(mul2(x1, s1), d[0], d[1]);
+                        x[e] = __fsub_rn(a[0], b[0]), x[e + 1] = __fsub_rn(a[1], b[1]);
+                        y[e] = __fadd_rn(c[0], d[0]), y[e + 1] = __fadd_rn(c[1], d[1]);
                     }
                 }
             }
